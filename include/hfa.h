@@ -1,7 +1,8 @@
 /*
  * hfa.h -- C ABI of libhfa: the single-token decode step and the multi-token verify
  * block of one Gemma-style attention layer on an NVIDIA GB300 (sm_103a), attention over
- * a quantised KV cache, and the layer's dense feed-forward half.
+ * a quantised KV cache, the layer's dense feed-forward half, and a paged 8-bit cache for
+ * serving (append, attention of ragged batches, read).
  *
  * Sources of the operation (hf2q documentation pages):
  *   "gemma4/gpu_full_attn.rs", encode_one_layer: the per-layer decode encoder --
@@ -29,7 +30,7 @@
  *     call launches nothing and touches no device memory.  The reason is available
  *     from hfa_last_error().
  *   - No entry point allocates device memory except the create functions
- *     (hfa_layer_create, hfa_tq_create, hfa_ffn_create).
+ *     (hfa_layer_create, hfa_tq_create, hfa_ffn_create, hfa_paged_create).
  *   - bf16 = IEEE bfloat16 bit pattern (uint16), row-major, densely packed.
  */
 #ifndef HFA_H
@@ -373,6 +374,136 @@ int hfa_ffn_stamp_rows(const hfa_ffn* ffn);
 /* the work plan: grid, batch tiles, then (k-splits, blocks per split, row groups per
  * stage, stages) of the gate/up and of the down projection; returns the count (10) */
 int hfa_ffn_plan_info(const hfa_ffn* ffn, int n, int* values);
+
+/*
+ * ---- A paged key/value cache in 8 bits, for serving (no counterpart on the pages, whose
+ * caches are one buffer per sequence: an interface addition of this library).
+ *
+ * The cache is a pool of pages of `page_size` tokens:
+ *   k_codes, v_codes    int8 [num_pages, nkv, page_size, hd], 16-byte aligned
+ *   k_scales, v_scales  f32  [num_pages, nkv]: one scale for each page and head;
+ *                       value = code * scale, codes in [-127, 127], scales finite and >= 0
+ * and a table int32 [batch, max_pages]: position p of sequence b is slot p % page_size of
+ * page table[b][p / page_size].  Entries of pages that hold no visible token are never
+ * read, so a sequence's pages behind its window may be given to another sequence.  Pages may
+ * be shared between sequences that only read them.
+ *
+ * A batch is ragged: `cu` int32 [batch + 1] (cu[0] = 0, not decreasing) gives the rows
+ * cu[b] .. cu[b+1] - 1 of sequence b in the packed row arrays [T, heads, hd], T = cu[batch].
+ * Sequences without rows are allowed (padding).  Arrays named *_host are host copies used
+ * for validation and launch sizes.  cu_dev always equals cu_host; a replayed graph may run
+ * with other start_dev, len_dev, count_dev and table_dev contents than those captured.  What
+ * the device finds wrong then (a position past the table, a page outside the pool) is
+ * skipped and recorded: hfa_paged_check_status reports it.
+ *
+ * The handle holds the descriptor, the norm weights and the rotation's frequencies, and
+ * nothing that a call writes but the error word: calls on one handle may overlap.
+ */
+typedef struct hfa_paged hfa_paged; /* opaque; owned by the library */
+typedef struct {
+  int num_heads, num_kv_heads; /* nh % nkv == 0, nh / nkv <= 8 */
+  int head_dim;                /* 64, 128 or 256 */
+  int page_size;               /* 16, 32, 64 or 128 */
+  int num_pages;               /* pages of the pool; num_pages * nkv * page_size < 2^31 */
+  int max_pages;               /* entries of a table row; max_pages * page_size <= 2^24 */
+  int window;                  /* 0: all earlier keys; W > 0: keys with P - W < p <= P */
+  float eps;                   /* of the norms */
+  float rope_theta;            /* as hfa_layer_desc */
+  float attn_scale;
+  float softcap;               /* 0 = off */
+  unsigned flags;              /* HFA_F_V_UNIT_NORM: V rows are unit-normed on the append;
+                                  HFA_F_BLOCK_BIDIR: every row of a sequence sees all of its
+                                  keys (not with a window) */
+} hfa_paged_desc;
+typedef struct {
+  int8_t* k_codes;
+  float* k_scales;
+  int8_t* v_codes;
+  float* v_scales;
+  const int32_t* table_dev;
+  const int32_t* table_host; /* the same table in host memory: hfa_paged_append needs it, the
+                                other calls ignore it */
+} hfa_pages;
+/* types of the row arrays */
+#define HFA_BF16 0
+#define HFA_F32 1
+
+/*
+ *   w_q_dev, w_k_dev  f32 [hd], copied: per-head RMSNorm of the q and k rows before the
+ *                     rotation (y = x * w / sqrt(mean(x^2) + eps)); NULL: no such norm
+ *   factors_host      f32 [hd/2] frequency factors (as hfa_set_rope_freq_factors), or NULL
+ * Synchronises `stream`.  Errors: HFA_EINVAL, HFA_EUNSUPPORTED (head dim, GQA group, page
+ * size, a pool past 32-bit rows), HFA_EDEVICE, HFA_ENOMEM, HFA_ECUDA; message via
+ * hfa_paged_last_error(NULL).
+ */
+hfa_status hfa_paged_create(const hfa_paged_desc* desc, const float* w_q_dev, const float* w_k_dev,
+                            const float* factors_host, void* stream, hfa_paged** out);
+hfa_status hfa_paged_destroy(hfa_paged* paged);              /* synchronises the device */
+const char* hfa_paged_last_error(const hfa_paged* paged);    /* NULL: this thread's last create error */
+/* Reads (synchronising `stream`) and clears the error word: HFA_OK, or HFA_EDEVICE when an
+ * earlier call met a position or page outside its range or gave up a bounded wait. */
+hfa_status hfa_paged_check_status(hfa_paged* paged, void* stream);
+
+/*
+ * Appends the rows of every sequence at positions start[b], start[b] + 1, ...:
+ *   q, k: norm (when the handle has its weight), then RoPE at the row's position;
+ *   v: unit norm with HFA_F_V_UNIT_NORM, else as it is;
+ *   k and v are coded into their pages, q is written to q_out.
+ * The scale of a page only grows while the page fills: with a the largest |value| a call
+ * writes into the page, the new scale is s' = max(s, a / 127), s counting as 0 when the
+ * call writes the page's first slot.  Where s' > s the codes c of the slots before the
+ * first written one become rint(c * (s / s')); written values become rint(y / s') (ties to
+ * even).  Slots behind the last written one are left as they are.  NaN is stored as 0 and an
+ * infinity as code +-127 (neither takes part in a); a scale below the smallest normal f32 is
+ * 0, its page all zeros.
+ *   start_dev / start_host  int32 [batch]
+ *   q_dev       [T, nh, hd], rows q_stride elements apart; NULL: no queries (q_out ignored)
+ *   k_dev,v_dev [T, nkv, hd], rows k_stride, v_stride elements apart (the heads of a row are
+ *               dense: all three may point into one packed projection output)
+ *   dtype       HFA_BF16 or HFA_F32, of q, k, v and q_out
+ *   q_out_dev   dense [T, nh, hd]; may be q_dev itself when that is dense
+ * Pointers and strides are multiples of 16 bytes.  No page may be written by two sequences
+ * of a call: such a table, and pages outside the pool, are refused (HFA_EINVAL), positions
+ * past the table with HFA_ERANGE.  batch <= 4096.
+ */
+hfa_status hfa_paged_append(hfa_paged* paged, void* stream, int batch, const int32_t* cu_dev,
+                            const int32_t* cu_host, const int32_t* start_dev,
+                            const int32_t* start_host, const void* q_dev, long long q_stride,
+                            const void* k_dev, long long k_stride, const void* v_dev,
+                            long long v_stride, int dtype, const hfa_pages* pages,
+                            void* q_out_dev);
+
+/*
+ * Attention of the newest rows of each sequence over its pages.  With len[b] tokens in the
+ * cache and n = cu[b+1] - cu[b] rows, row i is at position P = len[b] - n + i and sees
+ * positions p <= P (p > P - window with a window; all p < len[b] with HFA_F_BLOCK_BIDIR):
+ *   o = sum_p softmax_p(attn_scale * q . k_p [softcap]) v_p.
+ * A row that sees nothing (P < 0) gives zeros.
+ *   len_dev / len_host  int32 [batch], 0 <= len <= max_pages * page_size (HFA_ERANGE)
+ *   q_dev   [T, nh, hd], rows q_stride elements apart; o_dev dense [T, nh, hd]
+ *   dtype   of q and o.  HFA_F32 is for few rows: n * nh / nkv <= 8 in every sequence
+ *           (HFA_EUNSUPPORTED otherwise); with HFA_BF16 n is free.
+ *   workspace_dev  hfa_paged_workspace_bytes(paged, batch, T) bytes, 16-byte aligned, zero
+ *           before its first use; each call leaves it ready for the next.  Calls that share a
+ *           workspace must not overlap on the GPU.
+ */
+size_t hfa_paged_workspace_bytes(const hfa_paged* paged, int batch, int total_rows);
+hfa_status hfa_paged_attention(hfa_paged* paged, void* stream, int batch, const int32_t* cu_dev,
+                               const int32_t* cu_host, const int32_t* len_dev,
+                               const int32_t* len_host, const void* q_dev, long long q_stride,
+                               int dtype, const hfa_pages* pages, void* workspace_dev,
+                               size_t workspace_bytes, void* o_dev);
+
+/*
+ * Decodes positions start[b] .. start[b] + count[b] - 1 of each sequence into linear caches,
+ * the layout hfa_decode_step and hfa_attention_decode take: bf16(code * scale) of position
+ * p goes to slot p of k_cache_dev, v_cache_dev bf16 [batch, nkv, capacity, hd]; other slots
+ * are left as they are.  Errors: HFA_EINVAL, HFA_ERANGE (past the table or the capacity).
+ */
+hfa_status hfa_paged_read(hfa_paged* paged, void* stream, int batch, const int32_t* start_dev,
+                          const int32_t* start_host, const int32_t* count_dev,
+                          const int32_t* count_host, const hfa_pages* pages, int capacity,
+                          void* k_cache_dev, void* v_cache_dev);
 
 /*
  * Successor hint for decoding through a stack of layers (no counterpart on the pages,

@@ -1,0 +1,92 @@
+// hfa_paged.h -- the paged 8-bit key/value cache: launch arguments shared by its kernels
+// (k_paged.cu: append and read; k_paged_attn.cu: attention) and its C entries
+// (hfa_paged_api.cu).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace hfa {
+
+// The pool and the batch, as every kernel sees them.
+struct PagedView {
+  int8_t* k_codes;      // [num_pages, nkv, ps, hd]
+  int8_t* v_codes;
+  float* k_scales;      // [num_pages, nkv]
+  float* v_scales;
+  const int* table;     // [batch, max_pages]
+  int num_pages, max_pages;
+  int ps, ps_log2;      // page size
+  int nh, nkv, hd;
+  int batch;
+  unsigned* err;        // the handle's error word
+};
+
+struct PagedAppendArgs {
+  PagedView p;
+  const int* cu;        // [batch + 1]
+  const int* start;     // [batch]
+  int total;            // rows of the packed arrays (bounds the rows cu may name)
+  int single;           // every sequence has at most one row
+  int kv_per_cta;       // KV heads one CTA walks
+  const void *q, *k, *v;  // q nullable
+  long long q_stride, k_stride, v_stride;  // elements
+  void* q_out;
+  const float2* rope_g;  // [hd/2] (hi, lo) of theta^(-2i/hd) / (2 pi) / f_i
+  const float* w_q;     // nullable [hd]
+  const float* w_k;
+  int v_unit_norm;
+  float eps;
+};
+
+struct PagedReadArgs {
+  PagedView p;
+  const int* start;     // [batch]
+  const int* count;
+  int heads_per_cta;
+  int capacity;
+  __nv_bfloat16* k_cache;  // [batch, nkv, capacity, hd]
+  __nv_bfloat16* v_cache;
+};
+
+struct PagedAttnArgs {
+  PagedView p;
+  const int* cu;        // [batch + 1]
+  const int* len;       // [batch]
+  int total;            // rows
+  const void* q;
+  long long q_stride;   // elements
+  void* o;              // dense [total, nh, hd]
+  int f32;              // q and o are f32, else bf16
+  int window, bidir;
+  float qscale;         // scale * log2 e, or scale / softcap
+  float cap_log2;       // softcap * log2 e, 0 = none
+};
+
+cudaError_t launch_paged_append(const PagedAppendArgs& a, bool f32, int items, int sms, cudaStream_t s);
+cudaError_t launch_paged_read(const PagedReadArgs& a, int max_count, int sms, cudaStream_t s);
+cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s);
+
+// ------------------------------------------------------------------ device helpers
+#ifdef __CUDACC__
+// The sequence that owns slot i of a ragged index space: sequence b owns slots
+// base(b) .. base(b + 1) - 1 with base not decreasing and base(0) = 0.  One warp narrows the
+// range 32-fold a round (one load round trip up to 32 sequences, two up to 1024).
+template <class Base>
+__device__ __forceinline__ int find_seq(int batch, int i, const Base& base) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = batch;
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int off = lane * step;
+    const bool le = off < n && base(lo + off) <= i;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));
+    const int sel = (c > 0 ? c - 1 : 0) * step;
+    lo += sel;
+    n = min(step, n - sel);
+  }
+  return lo;
+}
+#endif
+
+}  // namespace hfa

@@ -1,0 +1,410 @@
+// hfa_paged_api.cu -- C entries of the paged 8-bit key/value cache: argument checks, launch
+// sizes and workspace layout (include/hfa.h).  Kernels: k_paged.cu, k_paged_attn.cu.
+#include <math.h>
+#include <stdarg.h>
+#include <stdio.h>
+
+#include <new>
+#include <vector>
+
+#include "hfa_common.cuh"
+#include "hfa_internal.h"
+#include "hfa_paged.h"
+
+struct hfa_paged {
+  hfa_paged_desc d;
+  int device = 0, num_sms = 0;
+  int ps_log2 = 0;
+  void* block = nullptr;  // error word, RoPE table, norm weights
+  unsigned* err = nullptr;
+  float2* rope_g = nullptr;
+  float* w_q = nullptr;
+  float* w_k = nullptr;
+  char msg[512] = {0};
+};
+
+namespace {
+
+thread_local char g_paged_error[512];
+
+hfa_status fail(hfa_paged* p, hfa_status st, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(p ? p->msg : g_paged_error, 512, fmt, ap);
+  va_end(ap);
+  return st;
+}
+
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+
+hfa_status validate(const hfa_paged_desc* d) {
+  if (!d) return fail(nullptr, HFA_EINVAL, "desc is NULL");
+  if (d->num_heads <= 0 || d->num_kv_heads <= 0 || d->num_heads % d->num_kv_heads)
+    return fail(nullptr, HFA_EINVAL, "num_heads=%d must be a positive multiple of num_kv_heads=%d",
+                d->num_heads, d->num_kv_heads);
+  if (d->num_heads / d->num_kv_heads > 8)
+    return fail(nullptr, HFA_EUNSUPPORTED, "GQA group %d > 8", d->num_heads / d->num_kv_heads);
+  if (d->num_kv_heads > 4096)
+    return fail(nullptr, HFA_EUNSUPPORTED, "num_kv_heads=%d > 4096", d->num_kv_heads);
+  if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256)
+    return fail(nullptr, HFA_EUNSUPPORTED, "head_dim=%d (supported: 64, 128, 256)", d->head_dim);
+  if (d->page_size != 16 && d->page_size != 32 && d->page_size != 64 && d->page_size != 128)
+    return fail(nullptr, HFA_EUNSUPPORTED, "page_size=%d (supported: 16, 32, 64, 128)", d->page_size);
+  if (d->num_pages <= 0 || d->max_pages <= 0)
+    return fail(nullptr, HFA_EINVAL, "num_pages=%d, max_pages=%d", d->num_pages, d->max_pages);
+  if ((long long)d->num_pages * d->num_kv_heads * d->page_size >= (1ll << 31))
+    return fail(nullptr, HFA_EUNSUPPORTED, "a pool of 2^31 rows or more");
+  if ((long long)d->max_pages * d->page_size > (1 << 24))
+    return fail(nullptr, HFA_EINVAL, "max_pages * page_size = %lld > 2^24",
+                (long long)d->max_pages * d->page_size);
+  if (d->flags & ~(HFA_F_V_UNIT_NORM | HFA_F_BLOCK_BIDIR))
+    return fail(nullptr, HFA_EINVAL, "flags 0x%x", d->flags);
+  if (d->window < 0) return fail(nullptr, HFA_EINVAL, "window=%d", d->window);
+  if (d->window > 0 && (d->flags & HFA_F_BLOCK_BIDIR))
+    return fail(nullptr, HFA_EINVAL, "HFA_F_BLOCK_BIDIR with a window");
+  if (!(d->eps >= 0.f) || !(d->rope_theta > 0.f) || !isfinite(d->eps) || !isfinite(d->rope_theta))
+    return fail(nullptr, HFA_EINVAL, "eps, rope_theta out of range");
+  if (!(d->attn_scale > 0.f) || !(d->softcap >= 0.f) || !isfinite(d->attn_scale) ||
+      !isfinite(d->softcap))
+    return fail(nullptr, HFA_EINVAL, "attn_scale, softcap out of range");
+  return HFA_OK;
+}
+
+// the current device is the handle's
+hfa_status check_device(hfa_paged* p) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail(p, HFA_EDEVICE, "no CUDA device: %s", cudaGetErrorString(e));
+  if (dev != p->device)
+    return fail(p, HFA_EDEVICE, "the current device is %d, the cache's %d", dev, p->device);
+  return HFA_OK;
+}
+
+hfa_status check_pages(hfa_paged* p, const hfa_pages* pg) {
+  if (!pg) return fail(p, HFA_EINVAL, "pages is NULL");
+  if (!pg->k_codes || !pg->k_scales || !pg->v_codes || !pg->v_scales || !pg->table_dev)
+    return fail(p, HFA_EINVAL, "a pool pointer or the table is NULL");
+  if (!aligned16(pg->k_codes) || !aligned16(pg->v_codes))
+    return fail(p, HFA_EINVAL, "the codes must be 16-byte aligned");
+  return HFA_OK;
+}
+
+// cu: 0 = cu[0] <= cu[1] ...; *total = cu[batch], *longest = the most rows of a sequence
+hfa_status check_cu(hfa_paged* p, int batch, const int32_t* cu, int* total, int* longest) {
+  if (cu[0] != 0) return fail(p, HFA_EINVAL, "cu[0]=%d, not 0", cu[0]);
+  int most = 0;
+  for (int b = 0; b < batch; ++b) {
+    const long long n = (long long)cu[b + 1] - cu[b];
+    if (n < 0 || n > (1 << 24)) return fail(p, HFA_EINVAL, "cu[%d]=%d after cu[%d]=%d", b + 1, cu[b + 1], b, cu[b]);
+    if (n > most) most = (int)n;
+  }
+  *total = cu[batch];
+  *longest = most;
+  return HFA_OK;
+}
+
+hfa::PagedView view(const hfa_paged* p, const hfa_pages* pg, int batch) {
+  hfa::PagedView v{};
+  v.k_codes = pg->k_codes;
+  v.v_codes = pg->v_codes;
+  v.k_scales = pg->k_scales;
+  v.v_scales = pg->v_scales;
+  v.table = pg->table_dev;
+  v.num_pages = p->d.num_pages;
+  v.max_pages = p->d.max_pages;
+  v.ps = p->d.page_size;
+  v.ps_log2 = p->ps_log2;
+  v.nh = p->d.num_heads;
+  v.nkv = p->d.num_kv_heads;
+  v.hd = p->d.head_dim;
+  v.batch = batch;
+  v.err = p->err;
+  return v;
+}
+
+// the pages a call writes: inside the pool, none twice
+hfa_status check_written(hfa_paged* p, int batch, const int32_t* cu, const int32_t* start,
+                         const int32_t* table) {
+  static thread_local std::vector<uint64_t> seen;  // a bit per page, all clear between calls
+  const int ps = p->d.page_size, np = p->d.num_pages;
+  const size_t words = ((size_t)np + 63) / 64;
+  try {
+    if (seen.size() < words) seen.resize(words, 0);
+  } catch (const std::bad_alloc&) {
+    return fail(p, HFA_ENOMEM, "host memory for the page check");
+  }
+  hfa_status st = HFA_OK;
+  int b = 0, bad_j = -1;
+  for (; b < batch && st == HFA_OK; ++b) {
+    const int n = cu[b + 1] - cu[b];
+    if (n == 0) continue;
+    const int32_t* row = table + (size_t)b * p->d.max_pages;
+    for (int j = start[b] / ps; j <= (start[b] + n - 1) / ps; ++j) {
+      const int pg = row[j];
+      if (pg < 0 || pg >= np) {
+        st = fail(p, HFA_EINVAL, "table[%d][%d]=%d outside the pool of %d pages", b, j, pg, np);
+        bad_j = j;
+        break;
+      }
+      const uint64_t bit = 1ull << (pg & 63);
+      if (seen[pg >> 6] & bit) {
+        st = fail(p, HFA_EINVAL, "page %d (table[%d][%d]) would be written twice", pg, b, j);
+        bad_j = j;
+        break;
+      }
+      seen[pg >> 6] |= bit;
+    }
+  }
+  for (int c = 0; c < b; ++c) {  // clear what was set
+    const int n = cu[c + 1] - cu[c];
+    if (n == 0) continue;
+    const int32_t* row = table + (size_t)c * p->d.max_pages;
+    const int end = (c == b - 1 && st != HFA_OK) ? bad_j - 1 : (start[c] + n - 1) / ps;
+    for (int j = start[c] / ps; j <= end; ++j) seen[row[j] >> 6] &= ~(1ull << (row[j] & 63));
+  }
+  return st;
+}
+
+}  // namespace
+
+extern "C" hfa_status hfa_paged_create(const hfa_paged_desc* desc, const float* w_q,
+                                       const float* w_k, const float* factors, void* stream,
+                                       hfa_paged** out) {
+  if (!out) return fail(nullptr, HFA_EINVAL, "out is NULL");
+  *out = nullptr;
+  const hfa_status st = validate(desc);
+  if (st != HFA_OK) return st;
+  const int hd = desc->head_dim;
+  if (factors)
+    for (int i = 0; i < hd / 2; ++i)
+      if (!(factors[i] > 0.f) || !isfinite(factors[i]))
+        return fail(nullptr, HFA_EINVAL, "factors[%d] must be finite and > 0", i);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail(nullptr, HFA_EDEVICE, "no CUDA device: %s", cudaGetErrorString(e));
+  int major = 0, minor = 0, sms = 0;
+  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+  cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (major != 10 || minor != 3 || sms <= 0)
+    return fail(nullptr, HFA_EDEVICE, "the device is sm_%d%d; libhfa is built for sm_103a only", major, minor);
+  hfa_paged* p = new (std::nothrow) hfa_paged();
+  if (!p) return fail(nullptr, HFA_ENOMEM, "host memory");
+  p->d = *desc;
+  p->device = dev;
+  p->num_sms = sms;
+  while ((1 << p->ps_log2) < desc->page_size) ++p->ps_log2;
+  // one allocation: 256 bytes of error word, then the table and the weights
+  float host[256 + 2 * 256] = {0};
+  for (int i = 0; i < hd / 2; ++i) {
+    double v = pow((double)desc->rope_theta, -2.0 * i / hd) / (2.0 * M_PI);
+    if (factors) v /= (double)factors[i];
+    host[2 * i] = (float)v;
+    host[2 * i + 1] = (float)(v - (double)host[2 * i]);
+  }
+  const size_t bytes = 256 + 3 * 256 * sizeof(float);
+  e = cudaMalloc(&p->block, bytes);
+  if (e != cudaSuccess) {
+    delete p;
+    return fail(nullptr, HFA_ENOMEM, "cudaMalloc: %s", cudaGetErrorString(e));
+  }
+  float* f = (float*)((char*)p->block + 256);
+  p->err = (unsigned*)p->block;
+  p->rope_g = (float2*)f;
+  p->w_q = w_q ? f + 256 : nullptr;
+  p->w_k = w_k ? f + 512 : nullptr;
+  cudaStream_t s = (cudaStream_t)stream;
+  e = cudaMemsetAsync(p->block, 0, bytes, s);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(f, host, hd * sizeof(float), cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess && w_q) e = cudaMemcpyAsync(p->w_q, w_q, hd * sizeof(float), cudaMemcpyDeviceToDevice, s);
+  if (e == cudaSuccess && w_k) e = cudaMemcpyAsync(p->w_k, w_k, hd * sizeof(float), cudaMemcpyDeviceToDevice, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) {
+    cudaFree(p->block);
+    delete p;
+    return fail(nullptr, HFA_ECUDA, "the handle's tables: %s", cudaGetErrorString(e));
+  }
+  *out = p;
+  return HFA_OK;
+}
+
+extern "C" hfa_status hfa_paged_destroy(hfa_paged* p) {
+  if (!p) return HFA_EINVAL;
+  cudaDeviceSynchronize();
+  cudaFree(p->block);
+  delete p;
+  return HFA_OK;
+}
+
+extern "C" const char* hfa_paged_last_error(const hfa_paged* p) { return p ? p->msg : g_paged_error; }
+
+extern "C" hfa_status hfa_paged_check_status(hfa_paged* p, void* stream) {
+  if (!p) return fail(nullptr, HFA_EINVAL, "the handle is NULL");
+  const hfa_status st = check_device(p);
+  if (st != HFA_OK) return st;
+  cudaStream_t s = (cudaStream_t)stream;
+  unsigned w = 0;
+  cudaError_t e = cudaMemcpyAsync(&w, p->err, sizeof w, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && w) e = cudaMemsetAsync(p->err, 0, sizeof w, s);
+  if (e != cudaSuccess) return fail(p, HFA_ECUDA, "reading the error word: %s", cudaGetErrorString(e));
+  if (w & hfa::kErrWaitTimeout) return fail(p, HFA_EDEVICE, "a bounded wait gave up");
+  if (w) return fail(p, HFA_EDEVICE, "a position or page outside its range was skipped");
+  return HFA_OK;
+}
+
+extern "C" hfa_status hfa_paged_append(hfa_paged* p, void* stream, int batch, const int32_t* cu_dev,
+                                       const int32_t* cu_host, const int32_t* start_dev,
+                                       const int32_t* start_host, const void* q, long long q_stride,
+                                       const void* k, long long k_stride, const void* v,
+                                       long long v_stride, int dtype, const hfa_pages* pages,
+                                       void* q_out) {
+  if (!p) return fail(nullptr, HFA_EINVAL, "the handle is NULL");
+  hfa_status st = check_pages(p, pages);
+  if (st != HFA_OK) return st;
+  if (batch < 1 || batch > 4096) return fail(p, HFA_EINVAL, "batch=%d", batch);
+  if (!cu_dev || !cu_host || !start_dev || !start_host || !pages->table_host)
+    return fail(p, HFA_EINVAL, "cu, start or the host table is NULL");
+  if (dtype != HFA_BF16 && dtype != HFA_F32) return fail(p, HFA_EINVAL, "dtype=%d", dtype);
+  int total = 0, longest = 0;
+  st = check_cu(p, batch, cu_host, &total, &longest);
+  if (st != HFA_OK) return st;
+  const hfa_paged_desc& d = p->d;
+  const int cap = d.max_pages * d.page_size;
+  for (int b = 0; b < batch; ++b)
+    if (start_host[b] < 0 || start_host[b] > cap - (cu_host[b + 1] - cu_host[b]))
+      return fail(p, HFA_ERANGE, "sequence %d: positions from %d, %d of them, outside a table of %d tokens",
+                  b, start_host[b], cu_host[b + 1] - cu_host[b], cap);
+  if (total == 0) return HFA_OK;
+  if (!k || !v || (q && !q_out)) return fail(p, HFA_EINVAL, "a row pointer is NULL");
+  const int per16 = dtype == HFA_F32 ? 4 : 8;
+  const long long qrow = (long long)d.num_heads * d.head_dim, kvrow = (long long)d.num_kv_heads * d.head_dim;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q ? q_out : nullptr) ||
+      (q && q_stride % per16) || k_stride % per16 || v_stride % per16)
+    return fail(p, HFA_EINVAL, "rows and strides must be multiples of 16 bytes");
+  if ((q && q_stride < qrow) || k_stride < kvrow || v_stride < kvrow)
+    return fail(p, HFA_EINVAL, "a row stride is shorter than the row");
+  if (q && q == q_out && q_stride != qrow)
+    return fail(p, HFA_EINVAL, "q_out may be q only when q is dense");
+  st = check_written(p, batch, cu_host, start_host, pages->table_host);
+  if (st != HFA_OK) return st;
+  st = check_device(p);
+  if (st != HFA_OK) return st;
+  hfa::PagedAppendArgs a{};
+  a.p = view(p, pages, batch);
+  a.cu = cu_dev;
+  a.start = start_dev;
+  a.total = total;
+  a.single = longest == 1;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out = q_out;
+  a.rope_g = p->rope_g;
+  a.w_q = p->w_q;
+  a.w_k = p->w_k;
+  a.v_unit_norm = (d.flags & HFA_F_V_UNIT_NORM) != 0;
+  a.eps = d.eps;
+  const int items = a.single ? batch : total / d.page_size + 2 * batch;
+  const cudaError_t e = hfa::launch_paged_append(a, dtype == HFA_F32, items, p->num_sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(p, HFA_ECUDA, "append launch: %s", cudaGetErrorString(e));
+  return HFA_OK;
+}
+
+extern "C" size_t hfa_paged_workspace_bytes(const hfa_paged* p, int batch, int total_rows) {
+  if (!p || batch < 1 || batch > 4096 || total_rows < 0) return 0;
+  return 256;
+}
+
+extern "C" hfa_status hfa_paged_attention(hfa_paged* p, void* stream, int batch,
+                                          const int32_t* cu_dev, const int32_t* cu_host,
+                                          const int32_t* len_dev, const int32_t* len_host,
+                                          const void* q, long long q_stride, int dtype,
+                                          const hfa_pages* pages, void* ws, size_t ws_bytes,
+                                          void* o) {
+  if (!p) return fail(nullptr, HFA_EINVAL, "the handle is NULL");
+  hfa_status st = check_pages(p, pages);
+  if (st != HFA_OK) return st;
+  if (batch < 1 || batch > 4096) return fail(p, HFA_EINVAL, "batch=%d", batch);
+  if (!cu_dev || !cu_host || !len_dev || !len_host) return fail(p, HFA_EINVAL, "cu or len is NULL");
+  if (dtype != HFA_BF16 && dtype != HFA_F32) return fail(p, HFA_EINVAL, "dtype=%d", dtype);
+  int total = 0, longest = 0;
+  st = check_cu(p, batch, cu_host, &total, &longest);
+  if (st != HFA_OK) return st;
+  const hfa_paged_desc& d = p->d;
+  const int cap = d.max_pages * d.page_size;
+  for (int b = 0; b < batch; ++b)
+    if (len_host[b] < 0 || len_host[b] > cap)
+      return fail(p, HFA_ERANGE, "len[%d]=%d outside a table of %d tokens", b, len_host[b], cap);
+  if (dtype == HFA_F32 && longest * (d.num_heads / d.num_kv_heads) > 8)
+    return fail(p, HFA_EUNSUPPORTED, "f32 queries: %d rows of a GQA group of %d (at most 8 together)",
+                longest, d.num_heads / d.num_kv_heads);
+  if (total == 0) return HFA_OK;
+  if (!q || !o || !ws) return fail(p, HFA_EINVAL, "q, o or the workspace is NULL");
+  if (!aligned16(q) || !aligned16(o) || !aligned16(ws) || q_stride % (dtype == HFA_F32 ? 4 : 8))
+    return fail(p, HFA_EINVAL, "q, o, the workspace and the row stride must be multiples of 16 bytes");
+  if (q_stride < (long long)d.num_heads * d.head_dim)
+    return fail(p, HFA_EINVAL, "the row stride is shorter than the row");
+  const size_t need = hfa_paged_workspace_bytes(p, batch, total);
+  if (ws_bytes < need) return fail(p, HFA_EINVAL, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+  st = check_device(p);
+  if (st != HFA_OK) return st;
+  hfa::PagedAttnArgs a{};
+  a.p = view(p, pages, batch);
+  a.cu = cu_dev;
+  a.len = len_dev;
+  a.total = total;
+  a.q = q;
+  a.q_stride = q_stride;
+  a.o = o;
+  a.f32 = dtype == HFA_F32;
+  a.window = d.window;
+  a.bidir = (d.flags & HFA_F_BLOCK_BIDIR) != 0;
+  const float log2e = 1.4426950408889634f;
+  a.qscale = d.softcap > 0.f ? d.attn_scale / d.softcap : d.attn_scale * log2e;
+  a.cap_log2 = d.softcap * log2e;
+  const cudaError_t e = hfa::launch_paged_attn(a, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(p, HFA_ECUDA, "attention launch: %s", cudaGetErrorString(e));
+  return HFA_OK;
+}
+
+extern "C" hfa_status hfa_paged_read(hfa_paged* p, void* stream, int batch, const int32_t* start_dev,
+                                     const int32_t* start_host, const int32_t* count_dev,
+                                     const int32_t* count_host, const hfa_pages* pages, int capacity,
+                                     void* k_cache, void* v_cache) {
+  if (!p) return fail(nullptr, HFA_EINVAL, "the handle is NULL");
+  hfa_status st = check_pages(p, pages);
+  if (st != HFA_OK) return st;
+  if (batch < 1 || batch > 4096) return fail(p, HFA_EINVAL, "batch=%d", batch);
+  if (!start_dev || !start_host || !count_dev || !count_host || !k_cache || !v_cache)
+    return fail(p, HFA_EINVAL, "a pointer argument is NULL");
+  if (!aligned16(k_cache) || !aligned16(v_cache))
+    return fail(p, HFA_EINVAL, "the caches must be 16-byte aligned");
+  if (capacity < 1) return fail(p, HFA_EINVAL, "capacity=%d", capacity);
+  const hfa_paged_desc& d = p->d;
+  const int cap = d.max_pages * d.page_size;
+  const int most = cap < capacity ? cap : capacity;
+  int longest = 0;
+  for (int b = 0; b < batch; ++b) {
+    if (count_host[b] < 0 || start_host[b] < 0 || count_host[b] > most || start_host[b] > most - count_host[b])
+      return fail(p, HFA_ERANGE, "sequence %d: positions from %d, %d of them, outside %d tokens", b,
+                  start_host[b], count_host[b], most);
+    if (count_host[b] > longest) longest = count_host[b];
+  }
+  if (longest == 0) return HFA_OK;
+  st = check_device(p);
+  if (st != HFA_OK) return st;
+  hfa::PagedReadArgs a{};
+  a.p = view(p, pages, batch);
+  a.start = start_dev;
+  a.count = count_dev;
+  a.capacity = capacity;
+  a.k_cache = (__nv_bfloat16*)k_cache;
+  a.v_cache = (__nv_bfloat16*)v_cache;
+  const cudaError_t e = hfa::launch_paged_read(a, longest, p->num_sms, (cudaStream_t)stream);
+  if (e != cudaSuccess) return fail(p, HFA_ECUDA, "read launch: %s", cudaGetErrorString(e));
+  return HFA_OK;
+}

@@ -32,6 +32,8 @@ HFA_F_DEBUG_TAPS = 0x8
 HFA_F_K_EQ_V = 0x10
 HFA_F_BLOCK_BIDIR = 0x20
 
+HFA_BF16, HFA_F32 = 0, 1
+
 
 class HfaError(RuntimeError):
     def __init__(self, status: int, message: str):
@@ -60,6 +62,20 @@ class hfa_attn_desc(ctypes.Structure):
 class hfa_ffn_desc(ctypes.Structure):
     _fields_ = [("hidden", ctypes.c_int), ("intermediate", ctypes.c_int), ("eps", ctypes.c_float),
                 ("scalar_len", ctypes.c_int), ("max_batch", ctypes.c_int)]
+
+
+class hfa_paged_desc(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int), ("num_kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("page_size", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("max_pages", ctypes.c_int), ("window", ctypes.c_int), ("eps", ctypes.c_float),
+                ("rope_theta", ctypes.c_float), ("attn_scale", ctypes.c_float),
+                ("softcap", ctypes.c_float), ("flags", ctypes.c_uint)]
+
+
+class hfa_pages(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("table_dev", ctypes.c_void_p), ("table_host", ctypes.c_void_p)]
 
 
 def attn_desc_for(w: wl.Workload) -> hfa_attn_desc:
@@ -164,6 +180,23 @@ def lib():
         L.hfa_ffn_stamp_rows.argtypes = [P]
         L.hfa_ffn_plan_info.restype = C
         L.hfa_ffn_plan_info.argtypes = [P, I, ctypes.POINTER(ctypes.c_int)]
+        LL, PD, PP = ctypes.c_longlong, ctypes.POINTER(hfa_paged_desc), ctypes.POINTER(hfa_pages)
+        L.hfa_paged_create.restype = C
+        L.hfa_paged_create.argtypes = [PD, P, P, P, P, ctypes.POINTER(P)]
+        L.hfa_paged_destroy.restype = C
+        L.hfa_paged_destroy.argtypes = [P]
+        L.hfa_paged_last_error.restype = ctypes.c_char_p
+        L.hfa_paged_last_error.argtypes = [P]
+        L.hfa_paged_check_status.restype = C
+        L.hfa_paged_check_status.argtypes = [P, P]
+        L.hfa_paged_append.restype = C
+        L.hfa_paged_append.argtypes = [P, P, I, P, P, P, P, P, LL, P, LL, P, LL, I, PP, P]
+        L.hfa_paged_workspace_bytes.restype = ctypes.c_size_t
+        L.hfa_paged_workspace_bytes.argtypes = [P, I, I]
+        L.hfa_paged_attention.restype = C
+        L.hfa_paged_attention.argtypes = [P, P, I, P, P, P, P, P, LL, I, PP, P, ctypes.c_size_t, P]
+        L.hfa_paged_read.restype = C
+        L.hfa_paged_read.argtypes = [P, P, I, P, P, P, P, PP, I, P, P]
         _lib = L
     return _lib
 
@@ -504,3 +537,172 @@ class Ffn:
             self.hfa_ffn_destroy()
         except Exception:
             pass
+
+
+class Pages:
+    """A page pool and a batch's table (hfa_pages): int8 codes [num_pages, nkv, page_size, hd],
+    f32 scales [num_pages, nkv], the int32 table [batch, max_pages] on the device and (for
+    appends) in host memory.  Keeps the tensors alive."""
+
+    def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                 v_scales: torch.Tensor, table: torch.Tensor, table_host: Optional[np.ndarray] = None):
+        for name, t, kind in (("k_codes", k_codes, torch.int8), ("v_codes", v_codes, torch.int8),
+                              ("k_scales", k_scales, torch.float32),
+                              ("v_scales", v_scales, torch.float32), ("table", table, torch.int32)):
+            if t.dtype != kind or not t.is_contiguous():
+                raise HfaError(HFA_EINVAL, f"{name} must be contiguous {kind}")
+        if k_codes.shape != v_codes.shape or k_codes.dim() != 4:
+            raise HfaError(HFA_EINVAL, "k_codes and v_codes are [num_pages, nkv, page_size, hd]")
+        if k_scales.shape != k_codes.shape[:2] or v_scales.shape != k_codes.shape[:2]:
+            raise HfaError(HFA_EINVAL, "the scales are [num_pages, nkv]")
+        if table.dim() != 2:
+            raise HfaError(HFA_EINVAL, "the table is [batch, max_pages]")
+        if table_host is not None:
+            table_host = np.ascontiguousarray(table_host, dtype=np.int32)
+            if table_host.shape != tuple(table.shape):
+                raise HfaError(HFA_EINVAL, "table and table_host have different shapes")
+        self.tensors = (k_codes, k_scales, v_codes, v_scales, table, table_host)
+        self.batch, self.max_pages = table.shape
+        self.shape = tuple(k_codes.shape)
+        self.c = hfa_pages(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
+                           v_scales.data_ptr(), table.data_ptr(),
+                           None if table_host is None else table_host.ctypes.data)
+        self.ref = ctypes.byref(self.c)
+
+
+class Paged:
+    """The paged 8-bit KV cache's descriptor, rotation and norms (hfa_paged_create ...)."""
+
+    def __init__(self, desc: hfa_paged_desc, w_q: Optional[torch.Tensor] = None,
+                 w_k: Optional[torch.Tensor] = None, rope_factors: Optional[np.ndarray] = None,
+                 stream=None):
+        self._h = ctypes.c_void_p()
+        for w in (w_q, w_k):
+            if w is not None and (w.dtype != torch.float32 or w.numel() != desc.head_dim or
+                                  not w.is_contiguous()):
+                raise HfaError(HFA_EINVAL, "w_q and w_k are f32 [head_dim]")
+        if rope_factors is not None:
+            rope_factors = np.ascontiguousarray(rope_factors, dtype=np.float32)
+            if rope_factors.size != desc.head_dim // 2:
+                raise HfaError(HFA_EINVAL, "rope_factors is [head_dim / 2]")
+        # a copy: later changes to the caller's structure do not reach the checks below
+        self.desc = hfa_paged_desc.from_buffer_copy(desc)
+        st = lib().hfa_paged_create(ctypes.byref(desc), _ptr(w_q), _ptr(w_k),
+                                    None if rope_factors is None else rope_factors.ctypes.data,
+                                    _stream_ptr(stream), ctypes.byref(self._h))
+        if st != HFA_OK:
+            raise HfaError(st, lib().hfa_paged_last_error(None).decode())
+        self._pool = (desc.num_pages, desc.num_kv_heads, desc.page_size, desc.head_dim)
+
+    def _check(self, st: int):
+        if st != HFA_OK:
+            raise HfaError(st, lib().hfa_paged_last_error(self._h).decode())
+
+    def _batch(self, ints, pages: Pages) -> list:
+        """Host int32 arrays of a call; the pool and the table fit the descriptor."""
+        if pages.shape != self._pool or pages.max_pages != self.desc.max_pages:
+            raise HfaError(HFA_EINVAL, f"a pool {pages.shape} with {pages.max_pages} table entries, "
+                                       f"the cache is {self._pool} with {self.desc.max_pages}")
+        return [np.ascontiguousarray(x, dtype=np.int32) for x in ints]
+
+    def _rows(self, x: torch.Tensor, heads: int, total: int, dtype=None):
+        """(data pointer, row stride) of a [total, heads, hd] array whose heads are dense."""
+        hd = self.desc.head_dim
+        if x.shape != (total, heads, hd) or (dtype is not None and x.dtype != dtype):
+            raise HfaError(HFA_EINVAL, f"rows {tuple(x.shape)} {x.dtype}, expected "
+                                       f"{(total, heads, hd)} {dtype or ''}")
+        st = x.stride()
+        if total and (st[2] != 1 or (heads > 1 and st[1] != hd)):
+            raise HfaError(HFA_EINVAL, "the heads of a row must be dense")
+        return x.data_ptr(), st[0] if total > 1 else heads * hd
+
+    @staticmethod
+    def _dtype(x: torch.Tensor) -> int:
+        if x.dtype == torch.bfloat16:
+            return HFA_BF16
+        if x.dtype == torch.float32:
+            return HFA_F32
+        raise HfaError(HFA_EINVAL, f"rows of {x.dtype}: bf16 or f32")
+
+    def hfa_paged_append(self, cu_dev: torch.Tensor, cu_host, start_dev: torch.Tensor, start_host,
+                         q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pages: Pages,
+                         q_out: Optional[torch.Tensor] = None, stream=None) -> None:
+        cu, start = self._batch((cu_host, start_host), pages)
+        batch, total = _ragged(cu, start, pages, cu_dev, start_dev)
+        dtype = self._dtype(k)
+        nh, nkv = self.desc.num_heads, self.desc.num_kv_heads
+        kp, ks = self._rows(k, nkv, total)
+        vp, vs = self._rows(v, nkv, total, k.dtype)
+        qp, qs, op = None, 0, None
+        if q is not None:
+            if q_out is None:
+                raise HfaError(HFA_EINVAL, "queries without q_out")
+            qp, qs = self._rows(q, nh, total, k.dtype)
+            op, os_ = self._rows(q_out, nh, total, k.dtype)
+            if os_ != nh * self.desc.head_dim:
+                raise HfaError(HFA_EINVAL, "q_out must be dense")
+        st = lib().hfa_paged_append(self._h, _stream_ptr(stream), batch, cu_dev.data_ptr(),
+                                    cu.ctypes.data, start_dev.data_ptr(), start.ctypes.data, qp, qs,
+                                    kp, ks, vp, vs, dtype, pages.ref, op)
+        self._check(st)
+
+    def hfa_paged_workspace_bytes(self, batch: int, total_rows: int) -> int:
+        return int(lib().hfa_paged_workspace_bytes(self._h, int(batch), int(total_rows)))
+
+    def hfa_paged_attention(self, cu_dev: torch.Tensor, cu_host, len_dev: torch.Tensor, len_host,
+                            q: torch.Tensor, pages: Pages, workspace: torch.Tensor, o: torch.Tensor,
+                            stream=None) -> torch.Tensor:
+        cu, lens = self._batch((cu_host, len_host), pages)
+        batch, total = _ragged(cu, lens, pages, cu_dev, len_dev)
+        nh = self.desc.num_heads
+        qp, qs = self._rows(q, nh, total)
+        op, os_ = self._rows(o, nh, total, q.dtype)
+        if os_ != nh * self.desc.head_dim:
+            raise HfaError(HFA_EINVAL, "o must be dense")
+        st = lib().hfa_paged_attention(self._h, _stream_ptr(stream), batch, cu_dev.data_ptr(),
+                                       cu.ctypes.data, len_dev.data_ptr(), lens.ctypes.data, qp, qs,
+                                       self._dtype(q), pages.ref, workspace.data_ptr(),
+                                       workspace.numel() * workspace.element_size(), op)
+        self._check(st)
+        return o
+
+    def hfa_paged_read(self, start_dev: torch.Tensor, start_host, count_dev: torch.Tensor, count_host,
+                       pages: Pages, k_cache: torch.Tensor, v_cache: torch.Tensor, stream=None) -> None:
+        start, count = self._batch((start_host, count_host), pages)
+        batch = start.size
+        if count.size != batch or pages.batch < batch or start_dev.numel() < batch or \
+                count_dev.numel() < batch or start_dev.dtype != torch.int32 or \
+                count_dev.dtype != torch.int32:
+            raise HfaError(HFA_EINVAL, "start, count and the table do not agree on the batch")
+        want = (batch, self.desc.num_kv_heads, k_cache.shape[2], self.desc.head_dim)
+        for c in (k_cache, v_cache):
+            if tuple(c.shape) != want or c.dtype != torch.bfloat16 or not c.is_contiguous():
+                raise HfaError(HFA_EINVAL, f"the caches are contiguous bf16 {want}")
+        self._check(lib().hfa_paged_read(self._h, _stream_ptr(stream), batch, start_dev.data_ptr(),
+                                         start.ctypes.data, count_dev.data_ptr(), count.ctypes.data,
+                                         pages.ref, int(k_cache.shape[2]), k_cache.data_ptr(),
+                                         v_cache.data_ptr()))
+
+    def hfa_paged_check_status(self, stream=None) -> None:
+        self._check(lib().hfa_paged_check_status(self._h, _stream_ptr(stream)))
+
+    def hfa_paged_destroy(self) -> None:
+        if self._h:
+            lib().hfa_paged_destroy(self._h)
+            self._h = ctypes.c_void_p()
+
+    def __del__(self):
+        try:
+            self.hfa_paged_destroy()
+        except Exception:
+            pass
+
+
+def _ragged(cu: np.ndarray, per: np.ndarray, pages: Pages, cu_dev: torch.Tensor,
+            per_dev: torch.Tensor):
+    """(batch, rows) of a ragged call, its arrays agreeing on the batch."""
+    batch = per.size
+    if batch < 1 or cu.size != batch + 1 or pages.batch < batch or cu_dev.numel() < batch + 1 or \
+            per_dev.numel() < batch or cu_dev.dtype != torch.int32 or per_dev.dtype != torch.int32:
+        raise HfaError(HFA_EINVAL, "cu, the lengths and the table do not agree on the batch")
+    return batch, int(cu[-1])
