@@ -405,7 +405,7 @@ typedef struct {
   int head_dim;                /* 64, 128 or 256 */
   int page_size;               /* 16, 32, 64 or 128 */
   int num_pages;               /* pages of the pool; num_pages * nkv * page_size < 2^31 */
-  int max_pages;               /* entries of a table row; max_pages * page_size <= 2^24 */
+  int max_pages;               /* entries of a table row; max_pages * page_size < 2^24 */
   int window;                  /* 0: all earlier keys; W > 0: keys with P - W < p <= P */
   float eps;                   /* of the norms */
   float rope_theta;            /* as hfa_layer_desc */

@@ -1,8 +1,9 @@
 // hfa_paged.h -- the paged 8-bit key/value cache: launch arguments shared by its kernels
-// (k_paged.cu: append and read; k_paged_attn.cu: attention) and its C entries
+// (k_paged.cu: append and read; k_paged_step.cu, k_paged_attn.cu: attention) and its C entries
 // (hfa_paged_api.cu).
 #pragma once
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -61,14 +62,39 @@ struct PagedAttnArgs {
   int window, bidir;
   float qscale;         // scale * log2 e, or scale / softcap
   float cap_log2;       // softcap * log2 e, 0 = none
+  int* tickets;         // [batch * nkv], zero between calls: parts of a unit that are done
+  float* records;       // [2 * kPagedMaxParts][kPagedStepRows][kPagedRecord(hd)]
 };
+
+// The step kernel (k_paged_step.cu) serves the sequences whose rows x heads of a KV head are
+// at most kPagedStepRows, on at most kPagedMaxParts CTAs.  A record holds one row's part of
+// the attention: O[hd], the maximum of s + log2 vs its weights refer to, the maximum of s,
+// the denominator, a pad.
+constexpr int kPagedStepRows = 8;
+constexpr int kPagedMaxParts = 320;
+__host__ __device__ constexpr int kPagedRecord(int hd) { return hd + 4; }
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, bool f32, int items, int sms, cudaStream_t s);
 cudaError_t launch_paged_read(const PagedReadArgs& a, int max_count, int sms, cudaStream_t s);
 cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s);
+// blocks: the 16-key blocks of the sequences it serves, times nkv; max_rows: their most rows x
+// heads of a KV head; tk, tv: byte views of the pools in boxes of 16 rows
+cudaError_t launch_paged_step(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                              long long blocks, int max_rows, int sms, cudaStream_t s);
 
 // ------------------------------------------------------------------ device helpers
 #ifdef __CUDACC__
+// four adjacent dims of an output row
+__device__ __forceinline__ void paged_store_o4(const PagedAttnArgs& a, int row, int h, int d, float4 v) {
+  const size_t at = ((size_t)row * a.p.nh + h) * a.p.hd + d;
+  if (a.f32) {
+    *reinterpret_cast<float4*>((float*)a.o + at) = v;
+  } else {
+    *reinterpret_cast<uint2*>((__nv_bfloat16*)a.o + at) =
+        make_uint2(pack_bf2(__float2bfloat16_rn(v.x), __float2bfloat16_rn(v.y)),
+                   pack_bf2(__float2bfloat16_rn(v.z), __float2bfloat16_rn(v.w)));
+  }
+}
 // The sequence that owns slot i of a ragged index space: sequence b owns slots
 // base(b) .. base(b + 1) - 1 with base not decreasing and base(0) = 0.  One warp narrows the
 // range 32-fold a round (one load round trip up to 32 sequences, two up to 1024).

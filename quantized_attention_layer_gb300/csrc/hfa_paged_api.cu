@@ -54,8 +54,8 @@ hfa_status validate(const hfa_paged_desc* d) {
     return fail(nullptr, HFA_EINVAL, "num_pages=%d, max_pages=%d", d->num_pages, d->max_pages);
   if ((long long)d->num_pages * d->num_kv_heads * d->page_size >= (1ll << 31))
     return fail(nullptr, HFA_EUNSUPPORTED, "a pool of 2^31 rows or more");
-  if ((long long)d->max_pages * d->page_size > (1 << 24))
-    return fail(nullptr, HFA_EINVAL, "max_pages * page_size = %lld > 2^24",
+  if ((long long)d->max_pages * d->page_size >= (1 << 24))
+    return fail(nullptr, HFA_EINVAL, "max_pages * page_size = %lld, not below 2^24",
                 (long long)d->max_pages * d->page_size);
   if (d->flags & ~(HFA_F_V_UNIT_NORM | HFA_F_BLOCK_BIDIR))
     return fail(nullptr, HFA_EINVAL, "flags 0x%x", d->flags);
@@ -163,6 +163,12 @@ hfa_status check_written(hfa_paged* p, int batch, const int32_t* cu, const int32
     for (int j = start[c] / ps; j <= end; ++j) seen[row[j] >> 6] &= ~(1ull << (row[j] & 63));
   }
   return st;
+}
+
+// workspace: [tickets, 256-byte aligned][records of the step kernel]
+size_t ticket_bytes(int batch, int nkv) { return ((size_t)batch * nkv * sizeof(int) + 255) / 256 * 256; }
+size_t record_bytes(int hd) {
+  return (size_t)2 * hfa::kPagedMaxParts * hfa::kPagedStepRows * hfa::kPagedRecord(hd) * sizeof(float);
 }
 
 }  // namespace
@@ -316,7 +322,8 @@ extern "C" hfa_status hfa_paged_append(hfa_paged* p, void* stream, int batch, co
 
 extern "C" size_t hfa_paged_workspace_bytes(const hfa_paged* p, int batch, int total_rows) {
   if (!p || batch < 1 || batch > 4096 || total_rows < 0) return 0;
-  return 256;
+  const size_t tickets = ticket_bytes(batch, p->d.num_kv_heads);
+  return tickets + record_bytes(p->d.head_dim);
 }
 
 extern "C" hfa_status hfa_paged_attention(hfa_paged* p, void* stream, int batch,
@@ -366,7 +373,36 @@ extern "C" hfa_status hfa_paged_attention(hfa_paged* p, void* stream, int batch,
   const float log2e = 1.4426950408889634f;
   a.qscale = d.softcap > 0.f ? d.attn_scale / d.softcap : d.attn_scale * log2e;
   a.cap_log2 = d.softcap * log2e;
-  const cudaError_t e = hfa::launch_paged_attn(a, (cudaStream_t)stream);
+  a.tickets = (int*)ws;
+  a.records = (float*)((char*)ws + ticket_bytes(batch, d.num_kv_heads));
+  // the sequences of few rows, and the others
+  const int G = d.num_heads / d.num_kv_heads;
+  long long blocks = 0;
+  int few = 0, many = 0;
+  for (int b = 0; b < batch; ++b) {
+    const int n = cu_host[b + 1] - cu_host[b];
+    if (n == 0) continue;
+    if ((long long)n * G > hfa::kPagedStepRows) {
+      ++many;
+      continue;
+    }
+    if (n * G > few) few = n * G;
+    const int lo = d.window ? len_host[b] - n - d.window + 1 : 0;
+    const int nb = (len_host[b] + 15) / 16 - (lo > 0 ? lo / 16 : 0);
+    blocks += (long long)(nb < 1 ? 1 : nb) * d.num_kv_heads;
+  }
+  cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e = cudaSuccess;
+  if (few) {
+    CUtensorMap tk, tv;
+    const long long rows = (long long)d.num_pages * d.num_kv_heads * d.page_size;
+    const int box = d.head_dim < 128 ? d.head_dim : 128;
+    if (hfa_encode_u8_map(&tk, pages->k_codes, rows, d.head_dim, box, 16) != HFA_OK ||
+        hfa_encode_u8_map(&tv, pages->v_codes, rows, d.head_dim, box, 16) != HFA_OK)
+      return fail(p, HFA_EINVAL, "cannot describe the pool to the TMA unit");
+    e = hfa::launch_paged_step(a, tk, tv, blocks, few, p->num_sms, s);
+  }
+  if (e == cudaSuccess && many) e = hfa::launch_paged_attn(a, s);
   if (e != cudaSuccess) return fail(p, HFA_ECUDA, "attention launch: %s", cudaGetErrorString(e));
   return HFA_OK;
 }

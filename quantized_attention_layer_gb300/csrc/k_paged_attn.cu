@@ -23,6 +23,7 @@ __global__ void __launch_bounds__(128) paged_attn_kernel(const PagedAttnArgs a) 
   if (row >= a.total) return;
   const int b = find_seq(p.batch, row, [&](int i) { return a.cu[i]; });
   const int n = a.cu[b + 1] - a.cu[b], len = a.len[b];
+  if (n * (p.nh / p.nkv) <= kPagedStepRows) return;  // the step kernel's
   const bool bad = len < 0 || len > p.max_pages * p.ps;
   if (bad && lane == 0) atomicOr(p.err, kErrBadPosition);
   const int P = len - n + row - a.cu[b];

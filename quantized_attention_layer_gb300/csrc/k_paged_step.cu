@@ -1,0 +1,560 @@
+// k_paged_step.cu -- attention of few rows (rows x query heads of a KV head <= 8: single
+// tokens, or a few at small groups) over the paged 8-bit cache.
+//
+//   s_p = scale ks[page(p)] sum_d q_d kc[p][d]   (softcap: cap tanh(s / cap)),
+//   o   = sum_p softmax(s)_p vs[page(p)] vc[p],   codes kc, vc, scales ks, vs per page and head.
+//
+// Memory-bound: every code is read once.  The keys of all (sequence, KV head) units are one
+// list of 16-key blocks (a block never straddles a page, so it has one K and one V scale),
+// dealt out in equal contiguous ranges over the CTAs whatever the lengths of the sequences.
+// Inside a CTA the warps take blocks in turn; each warp streams its own blocks through its
+// own ring of shared-memory slots by TMA (swizzled boxes of 16 rows), so no warp waits for
+// another until the range leaves a unit.  Table entries and scales are fetched 32 blocks at
+// a time, one block a lane, half a batch ahead of their use.
+//
+// Both products run on mma.sync m16n8k16 in fp16, which holds the codes exactly: a code
+// byte becomes fp16 by one byte permute and one subtract for two.  Query rows take MMA rows
+// 0..7 as hi(q 2^-e) and rows 8..15 as the remainder lo (22 bits together, 2^e restored in
+// the f32 score), the softmax weights likewise.  A K word read by ldmatrix holds four
+// adjacent dims of one key; the MMA's k index walks the dims in that order and the query
+// fragments follow it.  A V word read by ldmatrix.trans holds two adjacent dims of two keys:
+// the permute that widens it also splits even from odd dims, two n8 tiles.
+//
+// The running maximum is kept lazily: it moves (and the accumulators are rescaled) only when
+// a score exceeds it by 2^8, which a warp vote finds without any shuffle.  The V scale enters
+// in the exponent: weights are w = 2^(s + log2 vs - mw) with a maximum mw of their own, the
+// denominator l = sum 2^(s - m): fp16 weights then keep their bits whatever the pages' scales.
+#include "hfa_common.cuh"
+#include "hfa_internal.h"
+#include "hfa_paged.h"
+
+namespace hfa {
+namespace {
+
+template <int HD>
+struct StepCfg {
+  static constexpr int NC = 8;                           // warps of a CTA
+  static constexpr int CPS = HD == 256 ? 1 : 2;          // CTAs per SM
+  static constexpr int BOXW = HD < 128 ? HD : 128;       // bytes of a TMA box row
+  static constexpr int NBOX = HD / BOXW;
+  static constexpr int SWM = BOXW == 128 ? 7 : 3;        // swizzled row bits
+  static constexpr int TILE = 16 * HD;                   // codes of one block, K or V
+  static constexpr int SLOT = 2 * TILE;
+  static constexpr int KS = HD / 16;
+  static constexpr int RS = kPagedRecord(HD);            // record: O[HD], mw, m, l, pad
+  static constexpr int QF = KS * 32 * 16;                // query fragments
+  // the merge area: NC / 2 warps' records of R rows, or the merge weights (R x CTAs)
+  static constexpr int red_floats(int rows) {
+    return rows * (NC / 2 * RS > kPagedMaxParts ? NC / 2 * RS : kPagedMaxParts);
+  }
+  static constexpr int MAXNS = HD == 64 ? 6 : 4;
+};
+
+constexpr float kNoMax = -1e30f;  // "no score yet"; finite, so differences are never NaN
+constexpr float kLazy = 8.f;      // how far (log2) a score may exceed the running maximum
+
+struct Block {   // what a slot's reader needs to know of its block
+  float ks;      // K scale
+  float lvs;     // log2 of the V scale, -inf for 0
+  int key0;      // position of its first key; -1: nothing visible (no copy was issued)
+  int pad;
+};
+
+// shared address of byte `byte` of row `row` of a block's tile
+template <class Cfg>
+__device__ __forceinline__ uint32_t tile_addr(uint32_t tile, int row, int byte) {
+  const int box = byte / Cfg::BOXW, bb = byte - box * Cfg::BOXW;
+  const uint32_t lin = (uint32_t)(row * Cfg::BOXW + bb);
+  return tile + (uint32_t)(box * 16 * Cfg::BOXW) + (lin ^ (((lin >> 7) & Cfg::SWM) << 4));
+}
+
+// blocks of sequence b (per KV head): those that any of its rows sees, one (empty) block when
+// there is none, 0 when this kernel does not serve the sequence
+struct SeqPlan {
+  int row0, n, len, lo, blocks;  // first row, rows, keys, first block
+};
+__device__ __forceinline__ SeqPlan plan_seq(const PagedAttnArgs& a, int b, int G) {
+  SeqPlan s;
+  s.row0 = a.cu[b];
+  s.n = a.cu[b + 1] - s.row0;
+  s.len = a.len[b];
+  s.lo = 0;
+  s.blocks = 0;
+  if (s.n <= 0 || s.n * G > kPagedStepRows || s.row0 < 0 || s.row0 > a.total - s.n) return s;
+  if (s.len < 0 || s.len > a.p.max_pages * a.p.ps) {
+    atomicOr(a.p.err, kErrBadPosition);
+    s.len = 0;
+  }
+  // the first row's first key .. the last key
+  const int lo = a.window ? s.len - s.n - a.window + 1 : 0;
+  s.lo = lo > 0 ? lo >> 4 : 0;
+  s.blocks = ((s.len + 15) >> 4) - s.lo;
+  if (s.blocks < 1) s.blocks = 1;
+  return s;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
+    paged_step_kernel(const __grid_constant__ CUtensorMap tmk,
+                      const __grid_constant__ CUtensorMap tmv, const PagedAttnArgs a, int ns,
+                      int max_rows) {
+  using Cfg = StepCfg<HD>;
+  constexpr int NC = Cfg::NC, RS = Cfg::RS, KS = Cfg::KS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_align1024(smem_raw);
+  const PagedView& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int G = p.nh / p.nkv;
+  // layout: rings [NC][ns], query fragments, merge area, barriers, block records, prefix
+  uint8_t* ring = smem + warp * ns * Cfg::SLOT;
+  uint4* qf = reinterpret_cast<uint4*>(smem + NC * ns * Cfg::SLOT);
+  float* red = reinterpret_cast<float*>(qf + KS * 32);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(red + Cfg::red_floats(max_rows)) + warp * Cfg::MAXNS;
+  Block* recs = reinterpret_cast<Block*>(reinterpret_cast<uint64_t*>(red + Cfg::red_floats(max_rows)) +
+                                         NC * Cfg::MAXNS) + warp * Cfg::MAXNS;
+  int* s_misc = reinterpret_cast<int*>(recs - warp * Cfg::MAXNS + NC * Cfg::MAXNS);  // [8]
+  float* s_rowf = reinterpret_cast<float*>(s_misc + 8);                              // [8]
+  int* s_warp = reinterpret_cast<int*>(s_rowf + 8);                                  // [NC]
+  unsigned* pre = reinterpret_cast<unsigned*>(s_warp + NC);  // [batch + 1]: blocks (times KV heads) before each sequence
+
+  if (lane == 0) {
+    for (int i = 0; i < ns; ++i) mbar_init(&bars[i], 1);
+    fence_barrier_init();
+  }
+  // ------------------------------------------------------------------ prefix over the batch
+  {
+    const int per = (p.batch + NC * 32 - 1) / (NC * 32);
+    const int b0 = threadIdx.x * per;
+    unsigned sum = 0;
+    for (int i = 0; i < per; ++i)
+      if (b0 + i < p.batch) sum += plan_seq(a, b0 + i, G).blocks;
+    unsigned inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) s_warp[warp] = (int)inc;
+    __syncthreads();
+    unsigned before = inc - sum;
+    for (int w = 0; w < warp; ++w) before += (unsigned)s_warp[w];
+    for (int i = 0; i < per; ++i)
+      if (b0 + i < p.batch) {
+        pre[b0 + i] = before;
+        before += plan_seq(a, b0 + i, G).blocks;
+      }
+    if (threadIdx.x == NC * 32 - 1) pre[p.batch] = before;
+    __syncthreads();
+  }
+  const long long W = (long long)pre[p.batch] * p.nkv;  // all blocks
+  // CTAs at work: every warp has a block before another CTA joins
+  long long A = (W + NC - 1) / NC;
+  if (A > gridDim.x) A = gridDim.x;
+  if (blockIdx.x >= A) return;
+  const long long t0 = W * blockIdx.x / A, t1 = W * (blockIdx.x + 1) / A;
+
+  // the sequence that owns block index x = t / nkv-scaled prefix: largest b, pre[b] nkv <= t
+  auto seq_of = [&](long long tt) {
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((long long)pre[mid] * p.nkv <= tt) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+
+  // ------------------------------------------------------------------ this warp's blocks
+  const int count = (int)(t1 - t0 > warp ? (t1 - t0 - warp + NC - 1) / NC : 0);
+  // a batch of 32 blocks, one a lane: where it is and its scales
+  int pg_next = -2, row_next = 0, key_next = -1;  // page id (-2: none, -3: refused), TMA row
+  float ks_cur = 0.f, lvs_cur = 0.f, ks_next = 0.f, vs_next = 0.f;
+  int row_cur = 0, key_cur = -1;
+  int kvh_next = 0;
+  auto fetch_pages = [&](int k) {  // blocks k .. k + 31: table entries
+    pg_next = -2;
+    key_next = -1;
+    if (k + lane < count) {
+      const long long tt = t0 + warp + (long long)(k + lane) * NC;
+      const int b = seq_of(tt);
+      const SeqPlan s = plan_seq(a, b, G);
+      const long long u = tt - (long long)pre[b] * p.nkv;
+      kvh_next = (int)(u / s.blocks);
+      const int key0 = (s.lo + (int)(u - (long long)kvh_next * s.blocks)) << 4;
+      if (key0 < s.len) {
+        key_next = key0;
+        pg_next = __ldg(p.table + (size_t)b * p.max_pages + (key0 >> p.ps_log2));
+      }
+    }
+  };
+  auto fetch_scales = [&]() {
+    ks_next = vs_next = 0.f;
+    if (key_next >= 0) {
+      if ((unsigned)pg_next < (unsigned)p.num_pages) {
+        const size_t u = (size_t)pg_next * p.nkv + kvh_next;
+        ks_next = __ldg(p.k_scales + u);
+        vs_next = __ldg(p.v_scales + u);
+        row_next = (int)u * p.ps + (key_next & (p.ps - 1));
+      } else {
+        atomicOr(p.err, kErrBadPosition);
+        key_next = -1;
+      }
+    }
+  };
+  auto turn_batch = [&]() {
+    row_cur = row_next;
+    key_cur = key_next;
+    ks_cur = ks_next;
+    lvs_cur = vs_next > 0.f ? log2f(vs_next) : -INFINITY;
+  };
+  auto issue = [&](int k) {  // block k into slot k % ns
+    const int src = k & 31, st = k % ns;
+    const int key0 = __shfl_sync(0xffffffffu, key_cur, src);
+    const int row = __shfl_sync(0xffffffffu, row_cur, src);
+    const float ks = __shfl_sync(0xffffffffu, ks_cur, src);
+    const float lvs = __shfl_sync(0xffffffffu, lvs_cur, src);
+    if (lane == 0) {
+      recs[st].ks = ks;
+      recs[st].lvs = lvs;
+      recs[st].key0 = key0;
+      if (key0 >= 0) {
+        uint8_t* kt = ring + st * Cfg::SLOT;
+        mbar_arrive_expect_tx(&bars[st], Cfg::SLOT);
+#pragma unroll
+        for (int j = 0; j < Cfg::NBOX; ++j) {
+          tma_load_2d(kt + j * 16 * Cfg::BOXW, &tmk, &bars[st], j * Cfg::BOXW, row);
+          tma_load_2d(kt + Cfg::TILE + j * 16 * Cfg::BOXW, &tmv, &bars[st], j * Cfg::BOXW, row);
+        }
+      } else {
+        mbar_arrive(&bars[st]);
+      }
+    }
+  };
+  // the order in which slots are filled: batches turn at multiples of 32
+  int issued = 0;
+  auto advance = [&]() {
+    if (issued >= count) return;
+    if ((issued & 31) == 0) {
+      turn_batch();
+      fetch_pages(issued + 32);
+    } else if ((issued & 31) == 16) {
+      fetch_scales();
+    }
+    issue(issued);
+    ++issued;
+  };
+  fetch_pages(0);
+  fetch_scales();
+  for (int i = 0; i < ns; ++i) advance();
+
+  // ------------------------------------------------------------------ pieces of units
+  bool dead = false;  // a wait gave up: no more reads, the barriers still match
+  int k = 0;
+  long long at = t0;  // first block of the piece
+  while (at < t1) {
+    const int b = seq_of(at);
+    const SeqPlan sq = plan_seq(a, b, G);
+    const long long ub = (long long)pre[b] * p.nkv;
+    const int kvh = (int)((at - ub) / sq.blocks);
+    const long long u0 = ub + (long long)kvh * sq.blocks, u1 = u0 + sq.blocks;
+    const long long end = u1 < t1 ? u1 : t1;
+    const int rows = sq.n * G;
+    // query fragments: row r = token * G + head; warp r builds row r
+    for (int r = warp; r < kPagedStepRows; r += NC) {
+      // a lane holds quads lane, lane + 32, ... of the row; lanes past the row hold zeros
+      constexpr int Q = (HD + 127) / 128;
+      const int tok = r / G, h = kvh * G + r - tok * G;
+      const size_t qo = (size_t)(sq.row0 + tok) * a.q_stride + (size_t)h * HD;
+      float x[Q][4];
+      float top = 0.f;
+#pragma unroll
+      for (int j = 0; j < Q; ++j) {
+        const int d = 4 * (lane + 32 * j);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (r < rows && d < HD) {
+          if (a.f32) {
+            v = __ldg(reinterpret_cast<const float4*>((const float*)a.q + qo + d));
+          } else {
+            const uint2 w = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)a.q + qo + d));
+            v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
+                            __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
+          }
+        }
+        x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
+        top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+      }
+#pragma unroll
+      for (int of = 16; of > 0; of >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, of));
+      // 2^-e by its exponent bits: the row's largest component lands in [1, 8)
+      const uint32_t E = min(max((__float_as_uint(top) >> 23) & 255u, 1u), 252u);
+      const float down = __uint_as_float((254u - E) << 23);
+#pragma unroll
+      for (int j = 0; j < Q; ++j) {
+        const int quad = lane + 32 * j;
+        __half xh[4], xl[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) split_f16(x[j][i] * down, xh[i], xl[i]);
+        if (4 * quad < HD)
+          qf[(quad >> 2) * 32 + r * 4 + (quad & 3)] = make_uint4(
+              pack_h2(xh[0], xh[1]), pack_h2(xl[0], xl[1]), pack_h2(xh[2], xh[3]), pack_h2(xl[2], xl[3]));
+      }
+      if (lane == 0) s_rowf[r] = __uint_as_float(E << 23) * a.qscale;
+    }
+    __syncthreads();
+    // row g: its keys [lo, hi)
+    const float rowf = s_rowf[g];
+    const int P = sq.len - sq.n + g / G;
+    const int hi = g < rows ? (a.bidir ? sq.len : P + 1) : 0;
+    const int lo = a.window ? P - a.window + 1 : 0;
+    float m = kNoMax, mw = kNoMax, l = 0.f;
+    float o[KS][2][4];
+#pragma unroll
+    for (int c = 0; c < KS; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[c][0][e] = o[c][1][e] = 0.f;
+
+    for (; k < count && t0 + warp + (long long)k * NC < end; ++k) {
+      const int st = k % ns;
+      if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bars[st], (k / ns) & 1, p.err))) dead = true;
+      if (dead) continue;
+      const Block blk = recs[st];
+      if (blk.key0 >= 0) {
+        const uint32_t kt = smem_u32(ring + st * Cfg::SLOT), vt = kt + Cfg::TILE;
+        // S = Q K^T over 16 keys: tiles of keys 0..7 and 8..15
+        float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
+        const int mrow = ((lane >> 3) & 1) * 8 + (lane & 7), mch = lane >> 4;
+#pragma unroll
+        for (int c = 0; c < KS; c += 2) {
+          uint32_t w[4];
+          ldmatrix_x4(tile_addr<Cfg>(kt, mrow, 16 * (c + mch)), w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint4 qa = qf[(c + i) * 32 + lane];
+            const uint32_t A4[4] = {qa.x, qa.y, qa.z, qa.w};
+            const uint32_t x0 = w[2 * i] ^ 0x80808080u, x1 = w[2 * i + 1] ^ 0x80808080u;
+            mma_f16(s0, A4, u8x2_to_h2(x0, kSelLo), u8x2_to_h2(x0, kSelHi));
+            mma_f16(s1, A4, u8x2_to_h2(x1, kSelLo), u8x2_to_h2(x1, kSelHi));
+          }
+        }
+        const float f = rowf * blk.ks;
+        float s[4] = {(s0[0] + s0[2]) * f, (s0[1] + s0[3]) * f, (s1[0] + s1[2]) * f,
+                      (s1[1] + s1[3]) * f};
+        if (a.cap_log2 != 0.f) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[e] = a.cap_log2 * tanhf(s[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = blk.key0 + 2 * t + (e & 1) + 8 * (e >> 1);
+          if (key >= hi || key < lo) s[e] = -INFINITY;
+        }
+        const float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+        if (__any_sync(0xffffffffu, top > m + kLazy || top + blk.lvs > mw + kLazy)) {
+          float r = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 2));
+          const float mn = fmaxf(m, r), wn = fmaxf(mw, r + blk.lvs);
+          l *= exp2f(m - mn);
+          const float corr = exp2f(mw - wn);
+          m = mn;
+          mw = wn;
+#pragma unroll
+          for (int c = 0; c < KS; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              o[c][0][e] *= corr;
+              o[c][1][e] *= corr;
+            }
+        }
+        uint32_t PA[4];
+        {
+          const float shift = blk.lvs - mw;
+          __half ph[4], pl[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            l += ex2_approx(s[e] - m);
+            split_f16(ex2_approx(s[e] + shift), ph[e], pl[e]);
+          }
+          PA[0] = pack_h2(ph[0], ph[1]);
+          PA[1] = pack_h2(pl[0], pl[1]);
+          PA[2] = pack_h2(ph[2], ph[3]);
+          PA[3] = pack_h2(pl[2], pl[3]);
+        }
+#pragma unroll
+        for (int c = 0; c < KS; c += 2) {
+          uint32_t w[4];
+          ldmatrix_x4_trans(tile_addr<Cfg>(vt, mrow, 16 * (c + mch)), w[0], w[1], w[2], w[3]);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t x0 = w[2 * i] ^ 0x80808080u, x1 = w[2 * i + 1] ^ 0x80808080u;
+            mma_f16(o[c + i][0], PA, u8x2_to_h2(x0, 0x4240u), u8x2_to_h2(x1, 0x4240u));
+            mma_f16(o[c + i][1], PA, u8x2_to_h2(x0, 0x4341u), u8x2_to_h2(x1, 0x4341u));
+          }
+        }
+      }
+      // every lane's reads of the slot have fed the MMAs above: the slot may be refilled
+      __syncwarp();
+      advance();
+    }
+
+    // ---------------------------------------------------------------- the CTA's record
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    // dims 16 c + 4 t .. + 3 of row g
+    auto o4 = [&](int c) {
+      return make_float4(o[c][0][0] + o[c][0][2], o[c][1][0] + o[c][1][2], o[c][0][1] + o[c][0][3],
+                         o[c][1][1] + o[c][1][3]);
+    };
+    float* mine = red + (size_t)(warp % (NC / 2)) * rows * RS + g * RS;
+    if (warp >= NC / 2 && g < rows) {
+#pragma unroll
+      for (int c = 0; c < KS; ++c) *reinterpret_cast<float4*>(mine + 16 * c + 4 * t) = o4(c);
+      if (t == 0) *reinterpret_cast<float4*>(mine + HD) = make_float4(mw, m, l, 0.f);
+    }
+    __syncthreads();
+    if (warp < NC / 2) {
+      const float4 y = g < rows ? *reinterpret_cast<const float4*>(mine + HD)
+                                : make_float4(kNoMax, kNoMax, 0.f, 0.f);
+      __syncwarp();  // the four lanes of a row have read what one of them overwrites
+      const float wn = fmaxf(mw, y.x), mn = fmaxf(m, y.y);
+      const float fa = exp2f(mw - wn), fb = exp2f(y.x - wn);
+      if (g < rows) {
+#pragma unroll
+      for (int c = 0; c < KS; ++c) {
+        float4* q4 = reinterpret_cast<float4*>(mine + 16 * c + 4 * t);
+        const float4 u = o4(c), v = *q4;
+        *q4 = make_float4(u.x * fa + v.x * fb, u.y * fa + v.y * fb, u.z * fa + v.z * fb,
+                          u.w * fa + v.w * fb);
+      }
+      if (t == 0)
+        *reinterpret_cast<float4*>(mine + HD) =
+            make_float4(wn, mn, l * exp2f(m - mn) + y.z * exp2f(y.y - mn), 0.f);
+      }
+    }
+    __syncthreads();
+    const bool whole = at == u0 && end == u1;
+    float* part = a.records + ((size_t)blockIdx.x * 2 + (at == u0)) * kPagedStepRows * RS;
+    constexpr int Q4 = HD / 4;
+    for (int i = threadIdx.x; i < rows * Q4; i += NC * 32) {
+      const int r = i / Q4, d4 = i - r * Q4;
+      float wm[NC / 2], mm = kNoMax, wx = kNoMax, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < NC / 2; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>(red + ((size_t)w * rows + r) * RS + HD);
+        wm[w] = y.x;
+        wx = fmaxf(wx, y.x);
+        const float mn = fmaxf(mm, y.y);
+        ll = ll * exp2f(mm - mn) + y.z * exp2f(y.y - mn);
+        mm = mn;
+      }
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < NC / 2; ++w) {
+        const float f = exp2f(wm[w] - wx);
+        const float4 v = reinterpret_cast<const float4*>(red + ((size_t)w * rows + r) * RS)[d4];
+        acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+      }
+      if (whole) {
+        const float f = ll > 0.f ? exp2f(wx - mm) / ll : 0.f;
+        paged_store_o4(a, sq.row0 + r / G, kvh * G + r % G, 4 * d4,
+                       make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+      } else {
+        reinterpret_cast<float4*>(part + r * RS)[d4] = acc;
+        if (d4 == 0) *reinterpret_cast<float4*>(part + r * RS + HD) = make_float4(wx, mm, ll, 0.f);
+      }
+    }
+    if (!whole) {
+      // CTAs first .. last hold parts of this unit; the last to finish combines them
+      const int first = (int)(((u0 + 1) * A - 1) / W), last = (int)((u1 * A - 1) / W);
+      const int parts = last - first + 1;
+      const int unit = b * p.nkv + kvh;
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        s_misc[0] = atomicAdd(a.tickets + unit, 1) == parts - 1;
+        __threadfence();
+      }
+      __syncthreads();
+      if (s_misc[0]) {
+        if (threadIdx.x == 0) a.tickets[unit] = 0;
+        // record i of the unit: CTA first + i, its tail piece (slot 1) for i = 0
+        auto rec = [&](int i, int r) {
+          return a.records + (((size_t)(first + i) * 2 + (i == 0)) * kPagedStepRows + r) * RS;
+        };
+        float* wsm = red;  // [rows][parts]
+        for (int r = warp; r < rows; r += NC) {
+          float wx = kNoMax, mm = kNoMax;
+          for (int i = lane; i < parts; i += 32) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(rec(i, r) + HD));
+            wx = fmaxf(wx, y.x);
+            mm = fmaxf(mm, y.y);
+          }
+#pragma unroll
+          for (int of = 16; of > 0; of >>= 1) {
+            wx = fmaxf(wx, __shfl_xor_sync(0xffffffffu, wx, of));
+            mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, of));
+          }
+          float ll = 0.f;
+          for (int i = lane; i < parts; i += 32) {
+            const float4 y = __ldcg(reinterpret_cast<const float4*>(rec(i, r) + HD));
+            ll += y.z * exp2f(y.y - mm);
+            wsm[r * parts + i] = exp2f(y.x - wx);
+          }
+          ll = warp_sum(ll);
+          const float f = ll > 0.f ? exp2f(wx - mm) / ll : 0.f;
+          __syncwarp();
+          for (int i = lane; i < parts; i += 32) wsm[r * parts + i] *= f;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < rows * Q4; i += NC * 32) {
+          const int r = i / Q4, d4 = i - r * Q4;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+          for (int j = 0; j < parts; ++j) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(rec(j, r)) + d4);
+            const float f = wsm[r * parts + j];
+            acc.x += f * v.x, acc.y += f * v.y, acc.z += f * v.z, acc.w += f * v.w;
+          }
+          paged_store_o4(a, sq.row0 + r / G, kvh * G + r % G, 4 * d4, acc);
+        }
+      }
+    }
+    at = end;
+    // red and s_misc are next written behind the barrier that follows the next piece's
+    // query fragments, and qf only holds what every warp has finished with
+  }
+  // a warp that gave up: its copies still in flight land before the CTA may exit
+  if (dead) {
+    for (int i = k > ns ? k - ns : 0; i < issued; ++i) mbar_wait(&bars[i % ns], (i / ns) & 1, p.err);
+  }
+}
+
+template <int HD>
+cudaError_t launch_step_hd(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                           long long blocks, int max_rows, int sms, cudaStream_t s) {
+  using Cfg = StepCfg<HD>;
+  const size_t fixed = 1024 + Cfg::QF + (size_t)Cfg::red_floats(max_rows) * 4 +
+                       Cfg::NC * Cfg::MAXNS * (8 + sizeof(Block)) + (16 + Cfg::NC + a.p.batch + 1) * 4;
+  const size_t budget = (Cfg::CPS == 2 ? 113 : 226) * 1024;
+  int ns = (int)((budget - fixed) / (Cfg::NC * Cfg::SLOT));
+  if (ns > Cfg::MAXNS) ns = Cfg::MAXNS;
+  const size_t smem = fixed + (size_t)ns * Cfg::NC * Cfg::SLOT;
+  cudaError_t e = cudaFuncSetAttribute(paged_step_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  long long grid = (blocks + Cfg::NC - 1) / Cfg::NC;
+  if (grid > (long long)sms * Cfg::CPS) grid = (long long)sms * Cfg::CPS;
+  if (grid > kPagedMaxParts) grid = kPagedMaxParts;
+  if (grid < 1) grid = 1;
+  paged_step_kernel<HD><<<(unsigned)grid, Cfg::NC * 32, smem, s>>>(tk, tv, a, ns, max_rows);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_step(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
+                              long long blocks, int max_rows, int sms, cudaStream_t s) {
+  if (a.p.hd == 64) return launch_step_hd<64>(a, tk, tv, blocks, max_rows, sms, s);
+  if (a.p.hd == 128) return launch_step_hd<128>(a, tk, tv, blocks, max_rows, sms, s);
+  return launch_step_hd<256>(a, tk, tv, blocks, max_rows, sms, s);
+}
+
+}  // namespace hfa

@@ -133,16 +133,16 @@ def test_append_token_by_token_grows_the_scale():
 
 
 def test_append_far_positions():
-    # the angle of position 2^24 - 1, and of factors below 1
+    # the angle of the last position there can be, and of factors below 1
     rng = np.random.default_rng(8)
     hd, ps = 128, 128
-    mx = (1 << 24) // ps
+    mx = (1 << 24) // ps - 1
     table = np.full((1, mx), -1, dtype=np.int32)
     table[0, -1] = 1
     pool = Pool(ref.make_pool(rng, 2, 1, ps, hd), table)
     ff = np.full(hd // 2, 0.75, dtype=np.float32)
     p = make(1, 1, hd, ps, 2, mx, rope_factors=ff)
-    start = np.array([(1 << 24) - 3], dtype=np.int32)
+    start = np.array([mx * ps - 3], dtype=np.int32)
     cu = ref.ragged([3])
     x = draw_rows(rng, 3, 3, hd, torch.float32)
     xd = x.cuda()
