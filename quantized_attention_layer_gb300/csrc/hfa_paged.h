@@ -1,5 +1,5 @@
 // hfa_paged.h -- the paged 8-bit key/value cache: launch arguments shared by its kernels
-// (k_paged.cu: append and read; k_paged_step.cu, k_paged_attn.cu: attention) and its C entries
+// (k_paged.cu: append and read; k_paged_step.cu, k_paged_block.cu: attention) and its C entries
 // (hfa_paged_api.cu).
 #pragma once
 #include <cuda.h>
@@ -64,6 +64,7 @@ struct PagedAttnArgs {
   float cap_log2;       // softcap * log2 e, 0 = none
   int* tickets;         // [batch * nkv], zero between calls: parts of a unit that are done
   float* records;       // [2 * kPagedMaxParts][kPagedStepRows][kPagedRecord(hd)]
+  float* block_records;  // [CTAs][rows of a CTA][kPagedRecord(hd)], with splits > 1
 };
 
 // The step kernel (k_paged_step.cu) serves the sequences whose rows x heads of a KV head are
@@ -72,11 +73,17 @@ struct PagedAttnArgs {
 // the denominator, a pad.
 constexpr int kPagedStepRows = 8;
 constexpr int kPagedMaxParts = 320;
+constexpr int kPagedMaxSplits = 32;
 __host__ __device__ constexpr int kPagedRecord(int hd) { return hd + 4; }
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, bool f32, int items, int sms, cudaStream_t s);
 cudaError_t launch_paged_read(const PagedReadArgs& a, int max_count, int sms, cudaStream_t s);
-cudaError_t launch_paged_attn(const PagedAttnArgs& a, cudaStream_t s);
+// The block kernel (k_paged_block.cu) serves the others, paged_block_rows(hd) rows x heads and
+// paged_block_keys(hd) keys at a time.  slots: total * G / rows + batch; splits (at most
+// kPagedMaxSplits): CTAs that share the keys of an item.
+int paged_block_rows(int hd);
+int paged_block_keys(int hd);
+cudaError_t launch_paged_block(const PagedAttnArgs& a, int slots, int splits, cudaStream_t s);
 // blocks: the 16-key blocks of the sequences it serves, times nkv; max_rows: their most rows x
 // heads of a KV head; tk, tv: byte views of the pools in boxes of 16 rows
 cudaError_t launch_paged_step(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -1,5 +1,6 @@
 // hfa_paged_api.cu -- C entries of the paged 8-bit key/value cache: argument checks, launch
-// sizes and workspace layout (include/hfa.h).  Kernels: k_paged.cu, k_paged_attn.cu.
+// sizes and workspace layout (include/hfa.h).  Kernels: k_paged.cu,
+// k_paged_step.cu, k_paged_block.cu.
 #include <math.h>
 #include <stdarg.h>
 #include <stdio.h>
@@ -165,7 +166,14 @@ hfa_status check_written(hfa_paged* p, int batch, const int32_t* cu, const int32
   return st;
 }
 
-// workspace: [tickets, 256-byte aligned][records of the step kernel]
+// workspace: [tickets, 256-byte aligned][records of the step kernel][records of the block
+// kernel, when its (row tile, KV head) slots are few enough to be shared by several CTAs]
+long long block_slots(const hfa_paged_desc& d, int batch, int total) {
+  return (long long)total * (d.num_heads / d.num_kv_heads) / hfa::paged_block_rows(d.head_dim) + batch;
+}
+long long block_units(const hfa_paged_desc& d, int batch, int total) {
+  return block_slots(d, batch, total) * d.num_kv_heads;
+}
 size_t ticket_bytes(int batch, int nkv) { return ((size_t)batch * nkv * sizeof(int) + 255) / 256 * 256; }
 size_t record_bytes(int hd) {
   return (size_t)2 * hfa::kPagedMaxParts * hfa::kPagedStepRows * hfa::kPagedRecord(hd) * sizeof(float);
@@ -323,7 +331,13 @@ extern "C" hfa_status hfa_paged_append(hfa_paged* p, void* stream, int batch, co
 extern "C" size_t hfa_paged_workspace_bytes(const hfa_paged* p, int batch, int total_rows) {
   if (!p || batch < 1 || batch > 4096 || total_rows < 0) return 0;
   const size_t tickets = ticket_bytes(batch, p->d.num_kv_heads);
-  return tickets + record_bytes(p->d.head_dim);
+  const int G = p->d.num_heads / p->d.num_kv_heads;
+  size_t blocks = 0;
+  if ((long long)total_rows * G > hfa::kPagedStepRows &&
+      block_units(p->d, batch, total_rows) * 2 <= hfa::kPagedMaxParts)
+    blocks = (size_t)hfa::kPagedMaxParts * hfa::paged_block_rows(p->d.head_dim) *
+             hfa::kPagedRecord(p->d.head_dim) * sizeof(float);
+  return tickets + record_bytes(p->d.head_dim) + blocks;
 }
 
 extern "C" hfa_status hfa_paged_attention(hfa_paged* p, void* stream, int batch,
@@ -378,12 +392,17 @@ extern "C" hfa_status hfa_paged_attention(hfa_paged* p, void* stream, int batch,
   // the sequences of few rows, and the others
   const int G = d.num_heads / d.num_kv_heads;
   long long blocks = 0;
-  int few = 0, many = 0;
+  int few = 0;
+  long long items = 0, most_tiles = 0;  // of the block kernel
+  const int rows_per = hfa::paged_block_rows(d.head_dim), keys_per = hfa::paged_block_keys(d.head_dim);
   for (int b = 0; b < batch; ++b) {
     const int n = cu_host[b + 1] - cu_host[b];
     if (n == 0) continue;
     if ((long long)n * G > hfa::kPagedStepRows) {
-      ++many;
+      items += ((long long)n * G + rows_per - 1) / rows_per * d.num_kv_heads;
+      long long seen = len_host[b];
+      if (d.window && seen > (long long)d.window + rows_per / G) seen = (long long)d.window + rows_per / G;
+      if (seen / keys_per + 1 > most_tiles) most_tiles = seen / keys_per + 1;
       continue;
     }
     if (n * G > few) few = n * G;
@@ -402,7 +421,18 @@ extern "C" hfa_status hfa_paged_attention(hfa_paged* p, void* stream, int batch,
       return fail(p, HFA_EINVAL, "cannot describe the pool to the TMA unit");
     e = hfa::launch_paged_step(a, tk, tv, blocks, few, p->num_sms, s);
   }
-  if (e == cudaSuccess && many) e = hfa::launch_paged_attn(a, s);
+  if (e == cudaSuccess && items) {
+    const long long units = block_units(d, batch, total);
+    if (units * hfa::kPagedMaxSplits >= (1ll << 31)) return fail(p, HFA_EUNSUPPORTED, "too many row tiles");
+    a.block_records = (float*)((char*)a.records + record_bytes(d.head_dim));
+    // with fewer items than SMs, as many CTAs an item as fill the SMs and have a key tile each
+    long long splits = p->num_sms / items;
+    if (splits > hfa::kPagedMaxSplits) splits = hfa::kPagedMaxSplits;
+    if (splits > most_tiles) splits = most_tiles;
+    if (splits > hfa::kPagedMaxParts / units) splits = hfa::kPagedMaxParts / units;
+    if (splits < 1) splits = 1;
+    e = hfa::launch_paged_block(a, (int)block_slots(d, batch, total), (int)splits, s);
+  }
   if (e != cudaSuccess) return fail(p, HFA_ECUDA, "attention launch: %s", cudaGetErrorString(e));
   return HFA_OK;
 }

@@ -1,0 +1,745 @@
+// k_paged_block.cu -- attention of blocks of rows (verification blocks, prompt chunks, whole
+// prompts) over the paged 8-bit cache, on the 5th-generation tensor cores.
+//
+//   s_p = scale ks[page(p)] sum_d q_d kc[p][d]   (softcap: cap tanh(s / cap)),
+//   o   = sum_p softmax(s)_p vs[page(p)] vc[p],   codes kc, vc, scales ks, vs per page and head,
+// over the positions row i of a sequence's n rows sees: p <= P = len - n + i (all p < len when
+// bidirectional), p > P - window with a window.
+//
+// The rows of a KV head are its query heads of each token in turn (row = token G + head), so a
+// tile of 128 rows reads each key once for all of them.  One CTA takes QT tiles of 128 rows
+// (two at hd 64 and 128, one at hd 256, where O fills half of TMEM) and walks over tiles of
+// KT keys:
+//   S = Q Kc^T  (M = 128 rows, N = KT keys, K = hd)   fp16 in, f32 in TMEM
+//   O += P Vc   (M = 128 rows, N = hd, K = KT keys)   P fp16 in TMEM over S's own columns
+// The codes are exact in fp16.  Q is the bf16 row scaled by a power of two (exact but for parts
+// 2^-25 below the row's largest); the page's K scale multiplies the f32 scores 16 keys at a
+// time, its V scale enters the weights' exponent:
+//   w = 2^(s + log2 vs - mw), mw the running maximum of s + log2 vs, l = sum w / vs,
+// so that P <= 2^8 whatever the scales: rounding P to fp16 costs 2^-11 of a weight, below the
+// bf16 rounding of the output.  mw moves lazily, when a row exceeds it by 2^8; then the
+// thread that owns the row rescales its O in TMEM.
+//
+// Roles: a warpgroup per S buffer does the softmax (a thread owns a row: no shuffles), the
+// converter warps turn int8 codes into the fp16 operand tiles (global to registers a tile
+// ahead, widened by one permute and one subtract for two codes, stored in the 128-byte swizzled
+// order of the MMA; V is read in place as an MN-major operand), and one thread issues the
+// MMAs: while one S buffer is in its softmax the tensor cores work for the other.
+// Bound: per 128 x 128 scores at hd 128 the tensor cores need 1024 cycles and the shared memory
+// that feeds them about 1150; the softmax warps' issue slots come next.
+//
+// When there are fewer (sequence, KV head, row tile) items than SMs, S CTAs share an item, each
+// a contiguous part of its key tiles; a second kernel adds their records.
+#include "hfa_common.cuh"
+#include "hfa_internal.h"
+#include "hfa_paged.h"
+
+namespace hfa {
+namespace {
+
+template <int HD>
+struct BlockCfg {
+  static constexpr int QT = HD == 256 ? 1 : 2;    // row tiles of a CTA
+  static constexpr int ROWS = QT * 128;
+  static constexpr int KT = HD == 256 ? 64 : 128; // keys of a tile
+  static constexpr int NG = KT / 16;              // 16-key groups: one scale each
+  static constexpr int NCW = HD == 256 ? 8 : 4;   // converter warps
+  static constexpr int SMW = QT * 4;              // softmax warps
+  static constexpr int THREADS = (SMW + NCW + 1) * 32;
+  static constexpr int BOXES = HD / 64;
+  static constexpr int QBOX = 128 * 128;          // bytes of a 64-dim box of a row tile
+  static constexpr int QTILE = BOXES * QBOX;
+  static constexpr int KBOX = KT * 128;
+  static constexpr int KTILE = BOXES * KBOX;
+  static constexpr int NST = 2;                   // operand stages of K and of V
+  static constexpr int NSC = 4;                   // scale slots (see sc_full)
+  static constexpr int SMEM_OPS = QT * QTILE + 2 * NST * KTILE;
+  static constexpr size_t SMEM = 1024 + SMEM_OPS + ROWS * 4 + NSC * (NG * 12 + 16) + 256;
+  static constexpr int S_COLS = KT;
+  static constexpr int O_COL = 2 * KT;            // TMEM: S buffers, then O tiles
+  static constexpr int PER = KT * HD / 16 / (NCW * 32);  // 16-byte loads of a converter thread
+  static constexpr int CPR = HD / 16;                    // 16-byte chunks of a row
+  static constexpr int RPP = NCW * 32 / CPR;             // rows of one pass of the converters
+  static_assert(O_COL + QT * HD <= 512, "TMEM");
+  static_assert(RPP % 16 == 0 || 16 % RPP == 0, "a pass covers whole groups, or lies in one");
+  static_assert(SMEM <= 232448, "shared memory");
+};
+
+constexpr float kNoMax = -1e30f;
+constexpr float kLazy = 8.f;
+constexpr float kZeroLvs = -100.f;  // log2 vs of a page whose scale is 0 (its codes count as 0)
+
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24) | (b_mn ? 1u << 16 : 0u);
+}
+// D[tmem] (+)= A[tmem] * B[smem desc]^T
+__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                              uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// tanh to about 1e-7 absolute from one exponential and one reciprocal
+__device__ __forceinline__ float tanh_ex2(float x) {
+  const float e = ex2_approx(fminf(x, 20.f) * 2.885390082f);  // e^(2x); 20: tanh is 1
+  return 1.f - 2.f * rcp_approx(1.f + e);
+}
+
+// The keys the tile sees, and its rows' place: everything a role needs of its item.
+struct BlockItem {
+  int b, kvh, row0, n, len;   // sequence, KV head, first row of the packed arrays, rows, keys
+  int r0, rows;               // first (token, head) row of the CTA's tiles, rows in them
+  int lo, hi;                 // keys that some row sees
+  int t0, t1;                 // key tiles of this CTA
+};
+// lower and upper limit of the keys row r (token r / G) sees
+__device__ __forceinline__ int2 row_keys(const PagedAttnArgs& a, const BlockItem& it, int tok) {
+  const int P = it.len - it.n + tok;
+  const int hi = a.bidir ? it.len : P + 1;
+  const int lo = a.window ? P - a.window + 1 : 0;
+  return make_int2(lo > 0 ? lo : 0, hi > 0 ? hi : 0);
+}
+// false: the slot has no rows.  One warp calls it together.
+template <int HD>
+__device__ __forceinline__ bool block_item(const PagedAttnArgs& a, int splits, int bid, BlockItem* out) {
+  using Cfg = BlockCfg<HD>;
+  const PagedView& p = a.p;
+  const int G = p.nh / p.nkv;
+  BlockItem it;
+  const int split = bid % splits;
+  const int u = bid / splits;
+  it.kvh = u % p.nkv;
+  const int slot = u / p.nkv;
+  // sequence b owns slots cu[b] G / ROWS + b ..: n G rows need at most n G / ROWS + 1
+  auto base = [&](int i) { return (int)((long long)a.cu[i] * G / Cfg::ROWS) + i; };
+  it.b = find_seq(p.batch, slot, base);
+  it.row0 = a.cu[it.b];
+  it.n = a.cu[it.b + 1] - it.row0;
+  it.len = a.len[it.b];
+  if (it.n <= 0 || (long long)it.n * G <= kPagedStepRows || it.row0 < 0 || it.row0 > a.total - it.n) return false;
+  const int R = it.n * G;
+  const int tiles = (R + Cfg::ROWS - 1) / Cfg::ROWS;
+  const int i = slot - base(it.b);
+  if (i >= tiles) return false;
+  if (it.len < 0 || it.len > p.max_pages * p.ps) {
+    if ((threadIdx.x & 31) == 0) atomicOr(p.err, kErrBadPosition);
+    it.len = 0;
+  }
+  it.r0 = (tiles - 1 - i) * Cfg::ROWS;  // the longest rows first
+  it.rows = min(Cfg::ROWS, R - it.r0);
+  const int tok0 = it.r0 / G, tok1 = (it.r0 + it.rows - 1) / G;
+  const int2 k0 = row_keys(a, it, tok0), k1 = row_keys(a, it, tok1);
+  it.lo = k0.x;
+  it.hi = k1.y;
+  if (it.hi > it.len) it.hi = it.len;
+  const int ta = it.lo / Cfg::KT, tb = (it.hi + Cfg::KT - 1) / Cfg::KT;
+  const int nt = tb > ta ? tb - ta : 0;
+  const int per = (nt + splits - 1) / splits;
+  it.t0 = ta + min(split * per, nt);
+  it.t1 = ta + min((split + 1) * per, nt);
+  *out = it;
+  return true;
+}
+
+template <int HD>
+__global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
+    paged_block_kernel(const PagedAttnArgs a, int splits) {
+  using Cfg = BlockCfg<HD>;
+  constexpr int QT = Cfg::QT, KT = Cfg::KT, NG = Cfg::NG, NST = Cfg::NST, NSC = Cfg::NSC;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_align1024(smem_raw);
+  uint8_t* q_s = smem;
+  uint8_t* k_s = smem + QT * Cfg::QTILE;
+  uint8_t* v_s = k_s + NST * Cfg::KTILE;
+  float* s_rowf = reinterpret_cast<float*>(smem + Cfg::SMEM_OPS);  // [ROWS] qscale 2^e
+  float* s_ks = s_rowf + Cfg::ROWS;   // [NSC][NG] K scale, -1: the group is not visible
+  float* s_lvs = s_ks + NSC * NG;     // log2 of the V scale
+  float* s_ivs = s_lvs + NSC * NG;    // 1 / 2^(that)
+  int* s_flag = reinterpret_cast<int*>(s_ivs + NSC * NG);  // [NSC] some group is refused
+  uint64_t* bars = reinterpret_cast<uint64_t*>(s_flag + NSC);
+  uint64_t* q_full = bars;            // 1
+  uint64_t* k_full = bars + 1;        // [NST] converted K tiles
+  uint64_t* v_full = k_full + NST;
+  uint64_t* k_free = v_full + NST;    // [NST] the MMAs have read them
+  uint64_t* v_free = k_free + NST;
+  uint64_t* sc_full = v_free + NST;   // [NSC] scales.  Slot i of tile t + NSC is written once
+                                      // tile t + NSC - NST's S is done, hence after every
+                                      // softmax of tile t
+  uint64_t* s_full = sc_full + NSC;   // [2] S ready
+  uint64_t* p_full = s_full + 2;      // [2] P written
+  uint64_t* o_full = p_full + 2;      // [2] a row tile's last O += P V is complete
+  uint64_t* pv_done = o_full + 2;     // QT 1: each tile's O += P V is complete
+  uint64_t* drain = pv_done + 1;      // after an abort: what was issued is complete
+  volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 1);
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1) + 1;
+  BlockItem* s_item = reinterpret_cast<BlockItem*>(s_tmem + 1);
+
+  const PagedView& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.nh / p.nkv;
+  if (warp == 0) {
+    BlockItem it;
+    const bool on = block_item<HD>(a, splits, blockIdx.x, &it);
+    if (lane == 0) {
+      if (!on) it.rows = 0;
+      *s_item = it;
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      mbar_init(q_full, Cfg::SMW);
+      for (int i = 0; i < NST; ++i) {
+        mbar_init(&k_full[i], Cfg::NCW);
+        mbar_init(&v_full[i], Cfg::NCW);
+        mbar_init(&k_free[i], 1);
+        mbar_init(&v_free[i], 1);
+      }
+      for (int i = 0; i < NSC; ++i) mbar_init(&sc_full[i], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&s_full[i], 1);
+        mbar_init(&p_full[i], 4);
+        mbar_init(&o_full[i], 1);
+      }
+      mbar_init(pv_done, 1);
+      mbar_init(drain, 1);
+      *s_abort = 0;
+      fence_barrier_init();
+    }
+  }
+  __syncthreads();
+  const BlockItem it = *s_item;
+  if (it.rows == 0) return;
+  if (warp == 2) {
+    tmem_alloc(s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const int tiles = it.rows > 128 ? QT : 1;  // row tiles with rows
+  const int nt = it.t1 - it.t0;
+
+  if (warp < Cfg::SMW) {
+    // ================================================================== softmax warps
+    const int j = warp >> 2;  // row tile
+    const int quad = warp & 3;
+    // ---- queries: a warp's 32 rows, CPR2 lanes a row with 8 dims each
+    {
+      constexpr int L = HD / 8 < 32 ? HD / 8 : 32;  // lanes of a row
+      constexpr int RPI = 32 / L;                   // rows at once
+      const int c = lane % L;
+#pragma unroll 4
+      for (int i = 0; i < 32 / RPI; ++i) {
+        const int r = quad * 32 + i * RPI + lane / L;  // row of the tile
+        const int R = it.r0 + j * 128 + r;
+        const bool on = j * 128 + r < it.rows;
+        uint4 w = make_uint4(0u, 0u, 0u, 0u);
+        if (on) {
+          const int tok = R / G, h = it.kvh * G + R - tok * G;
+          w = __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
+                                                   (size_t)(it.row0 + tok) * a.q_stride +
+                                                   (size_t)h * HD + 8 * c));
+        }
+        // largest exponent of the row (bf16 exponent bits of either half)
+        uint32_t e = 0;
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) e = max(e, max((ww[x] >> 7) & 255u, (ww[x] >> 23) & 255u));
+#pragma unroll
+        for (int o = 1; o < L; o <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+        e = min(max(e, 1u), 252u);
+        const float down = __uint_as_float((254u - e) << 23);
+        uint32_t hw[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          hw[x] = pack_h2(__float2half_rn(__uint_as_float(ww[x] << 16) * down),
+                          __float2half_rn(__uint_as_float(ww[x] & 0xffff0000u) * down));
+        const int box = c >> 3, ch = c & 7;
+        *reinterpret_cast<uint4*>(q_s + j * Cfg::QTILE + box * Cfg::QBOX + r * 128 +
+                                  ((ch ^ (r & 7)) << 4)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+        if (c == 0) s_rowf[j * 128 + r] = __uint_as_float(e << 23) * a.qscale;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+    }
+    // ---- this thread's row
+    const int r = quad * 32 + lane;
+    const bool on = j * 128 + r < it.rows;
+    const int tok = (it.r0 + j * 128 + r) / G;
+    int2 lim = on ? row_keys(a, it, tok) : make_int2(0, 0);
+    if (lim.y > it.len) lim.y = it.len;
+    // keys that every row of the warp sees: [wlo, whi)
+    int wlo = lim.x, whi = on ? lim.y : 0x7fffffff;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      wlo = max(wlo, __shfl_xor_sync(0xffffffffu, wlo, o));
+      whi = min(whi, __shfl_xor_sync(0xffffffffu, whi, o));
+    }
+    const float rowf = s_rowf[j * 128 + r];  // written by this warp
+    const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
+    float mw = kNoMax, l = 0.f;
+    bool ok = true;
+    const int nts = j < tiles ? nt : 0;
+    for (int i = 0; i < nts; ++i) {
+      const int sb = QT == 2 ? j : i & 1;               // S buffer
+      const int ph = QT == 2 ? i & 1 : (i >> 1) & 1;    // its phase
+      const int sc = i % NSC;
+      const int key0 = (it.t0 + i) * KT;
+      const uint32_t t_s = t_lane + sb * Cfg::S_COLS;
+      const uint32_t t_o = t_lane + Cfg::O_COL + j * HD;
+      ok = mbar_wait(&sc_full[sc], (i / NSC) & 1, p.err, (const volatile int*)s_abort) &&
+           mbar_wait(&s_full[sb], ph, p.err, (const volatile int*)s_abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        *s_abort = 1;
+        break;
+      }
+      tc_fence_after();
+      const float* ks = s_ks + sc * NG;
+      const float* lvs = s_lvs + sc * NG;
+      const float* ivs = s_ivs + sc * NG;
+      const bool masked = key0 < wlo || key0 + KT > whi || s_flag[sc];
+      // ---- maximum of s + log2 vs
+      float top = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < NG / 2; ++c) {
+        uint32_t x[2][16];
+        tmem_ld16_nowait(t_s + 32 * c, x[0]);
+        tmem_ld16_nowait(t_s + 32 * c + 16, x[1]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int gr = 2 * c + h;
+          float gm = -INFINITY;
+          if (!masked) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) gm = fmaxf(gm, __uint_as_float(x[h][e]));
+          } else if (ks[gr] >= 0.f) {
+            const int k0 = key0 + 16 * gr;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (k0 + e >= lim.x && k0 + e < lim.y) gm = fmaxf(gm, __uint_as_float(x[h][e]));
+          }
+          if (gm != -INFINITY) {
+            float s = gm * (ks[gr] * rowf);
+            if (a.cap_log2 != 0.f) s = a.cap_log2 * tanh_ex2(s);
+            top = fmaxf(top, s + lvs[gr]);
+          }
+        }
+      }
+      // ---- the maximum moves: O follows
+      if (__any_sync(0xffffffffu, top > mw + kLazy)) {
+        const float mn = fmaxf(mw, top);
+        const float corr = exp2f(mw - mn);
+        l *= corr;
+        mw = mn;
+        if (i > 0) {
+          if (QT == 1) {  // S of this tile was issued before the last P V
+            ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (i - 1) & 1, p.err, (const volatile int*)s_abort));
+            if (!ok) {
+              *s_abort = 1;
+              break;
+            }
+            tc_fence_after();
+          }
+#pragma unroll 2
+          for (int c = 0; c < HD / 16; ++c) {
+            uint32_t x[16];
+            tmem_ld16_nowait(t_o + 16 * c, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * corr);
+            tmem_st16(t_o + 16 * c, x);
+          }
+          tmem_wait_st();
+        }
+      }
+      // ---- weights, over the scores' own columns
+#pragma unroll
+      for (int c = 0; c < NG / 2; ++c) {
+        uint32_t x[2][16], w[16];
+        tmem_ld16_nowait(t_s + 32 * c, x[0]);
+        tmem_ld16_nowait(t_s + 32 * c + 16, x[1]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int gr = 2 * c + h;
+          const float kq = ks[gr] * rowf, sh = lvs[gr] - mw;
+          float2 sum = make_float2(0.f, 0.f);
+          const int k0 = key0 + 16 * gr;
+          const bool none = masked && ks[gr] < 0.f;
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) {
+            float2 s = make_float2(__uint_as_float(x[h][e]), __uint_as_float(x[h][e + 1]));
+            if (a.cap_log2 == 0.f) {
+              s = fma2(s, make_float2(kq, kq), make_float2(sh, sh));
+            } else {
+              s = mul2(s, make_float2(kq, kq));
+              s.x = a.cap_log2 * tanh_ex2(s.x) + sh;
+              s.y = a.cap_log2 * tanh_ex2(s.y) + sh;
+            }
+            s.x = ex2_approx(s.x);
+            s.y = ex2_approx(s.y);
+            if (masked) {
+              if (none || k0 + e < lim.x || k0 + e >= lim.y) s.x = 0.f;
+              if (none || k0 + e + 1 < lim.x || k0 + e + 1 >= lim.y) s.y = 0.f;
+            }
+            sum = add2(sum, s);
+            w[8 * h + (e >> 1)] = pack_h2(__float2half_rn(s.x), __float2half_rn(s.y));
+          }
+          l += (sum.x + sum.y) * ivs[gr];
+        }
+        tmem_st16(t_s + 16 * c, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[sb]);
+    }
+    // ---- the rows' output
+    if (ok && nts > 0) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&o_full[j], 0, p.err, (const volatile int*)s_abort));
+      if (!ok) *s_abort = 1;
+    }
+    tc_fence_after();
+    if (ok) {
+      const uint32_t t_o = t_lane + Cfg::O_COL + j * HD;
+      if (splits == 1) {
+        const float f = l > 0.f ? 1.f / l : 0.f;
+        const int R = it.r0 + j * 128 + r;
+        __nv_bfloat16* dst = (__nv_bfloat16*)a.o +
+                             ((size_t)(it.row0 + tok) * p.nh + it.kvh * G + (R - tok * G)) * HD;
+#pragma unroll 2
+        for (int c = 0; c < HD / 16; ++c) {
+          uint32_t x[16], w[8];
+          if (nts > 0) {
+            tmem_ld16_nowait(t_o + 16 * c, x);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = 0u;
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            w[e] = pack_bf2(__float2bfloat16_rn(__uint_as_float(x[2 * e]) * f),
+                            __float2bfloat16_rn(__uint_as_float(x[2 * e + 1]) * f));
+          if (on) {
+            reinterpret_cast<uint4*>(dst + 16 * c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(dst + 16 * c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+      } else {
+        float* rec = a.block_records + ((size_t)blockIdx.x * Cfg::ROWS + j * 128 + r) * kPagedRecord(HD);
+        if (nts > 0) {
+#pragma unroll 2
+          for (int c = 0; c < HD / 16; ++c) {
+            uint32_t x[16];
+            tmem_ld16_nowait(t_o + 16 * c, x);
+            tmem_wait_ld();
+            if (on) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                reinterpret_cast<uint4*>(rec + 16 * c)[e] =
+                    make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+            }
+          }
+        }
+        if (on) *reinterpret_cast<float4*>(rec + HD) = make_float4(mw, l, 0.f, 0.f);
+      }
+    }
+  } else if (warp < Cfg::SMW + Cfg::NCW) {
+    // ================================================================== converter warps
+    const int ct = threadIdx.x - Cfg::SMW * 32;
+    const int chunk = ct % Cfg::CPR, rr = ct / Cfg::CPR;
+    constexpr int PER = Cfg::PER;
+    // lane i < NG: the first row of group i of a tile in the pools, -1 when nothing of it is
+    // read (outside the visible keys), -2 for a refused page; and its scales
+    auto group_row = [&](int i) {
+      const int k0 = (it.t0 + i) * KT + 16 * lane;
+      if (i >= nt || lane >= NG || k0 >= it.hi || k0 + 16 <= it.lo) return -1;
+      const int pg = __ldg(p.table + (size_t)it.b * p.max_pages + (k0 >> p.ps_log2));
+      if ((unsigned)pg >= (unsigned)p.num_pages) return -2;
+      return (pg * p.nkv + it.kvh) * p.ps + (k0 & (p.ps - 1));
+    };
+    auto load = [&](const int8_t* codes, int grow, uint4 (&w)[PER]) {
+#pragma unroll
+      for (int x = 0; x < PER; ++x) {
+        const int row = x * Cfg::RPP + rr;
+        const int base = __shfl_sync(0xffffffffu, grow, row >> 4);
+        w[x] = base >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + ((size_t)base + (row & 15)) * HD) + chunk)
+                         : make_uint4(0u, 0u, 0u, 0u);
+      }
+    };
+    // 16 codes -> 32 bytes of the swizzled fp16 tile: chunks 2 (chunk % 4), + 1 of box chunk / 4
+    auto store = [&](uint8_t* tile, const uint4 (&w)[PER]) {
+      uint8_t* box = tile + (chunk >> 2) * Cfg::KBOX;
+      const int c0 = 2 * (chunk & 3);
+#pragma unroll
+      for (int x = 0; x < PER; ++x) {
+        const int row = x * Cfg::RPP + rr;
+        const uint32_t u[4] = {w[x].x ^ 0x80808080u, w[x].y ^ 0x80808080u, w[x].z ^ 0x80808080u,
+                               w[x].w ^ 0x80808080u};
+        *reinterpret_cast<uint4*>(box + row * 128 + ((c0 ^ (row & 7)) << 4)) =
+            make_uint4(u8x2_to_h2(u[0], kSelLo), u8x2_to_h2(u[0], kSelHi), u8x2_to_h2(u[1], kSelLo),
+                       u8x2_to_h2(u[1], kSelHi));
+        *reinterpret_cast<uint4*>(box + row * 128 + (((c0 + 1) ^ (row & 7)) << 4)) =
+            make_uint4(u8x2_to_h2(u[2], kSelLo), u8x2_to_h2(u[2], kSelHi), u8x2_to_h2(u[3], kSelLo),
+                       u8x2_to_h2(u[3], kSelHi));
+      }
+    };
+    uint4 kw[PER], vw[PER];
+    int grow = group_row(0);
+    int grow1 = group_row(1);
+    load(p.k_codes, grow, kw);
+    load(p.v_codes, grow, vw);
+    float ks = 0.f, vs = 0.f;
+    auto scales = [&](int gr) {
+      ks = vs = 0.f;
+      if (gr >= 0) {
+        ks = __ldg(p.k_scales + gr / p.ps);
+        vs = __ldg(p.v_scales + gr / p.ps);
+      }
+    };
+    const bool lead = warp == Cfg::SMW;
+    scales(grow);
+    for (int i = 0; i < nt; ++i) {
+      const int st = i % NST, sc = i % NSC;
+      const uint32_t ph = ((i / NST) & 1) ^ 1;
+      bool ok = i < NST || mbar_wait(&k_free[st], ph, p.err, (const volatile int*)s_abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        *s_abort = 1;
+        break;
+      }
+      if (lead) {
+        const bool bad = grow == -2;
+        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, kErrBadPosition);
+        if (lane < NG) {
+          s_ks[sc * NG + lane] = grow >= 0 ? ks : -1.f;
+          const float lv = vs > 0.f ? log2f(vs) : kZeroLvs;
+          s_lvs[sc * NG + lane] = lv;
+          s_ivs[sc * NG + lane] = vs > 0.f ? 1.f / vs : 1.2676506e30f;  // 2^100
+        }
+        const bool any_bad = __any_sync(0xffffffffu, bad);
+        if (lane == 0) s_flag[sc] = any_bad;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sc_full[sc]);
+      }
+      store(k_s + st * Cfg::KTILE, kw);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&k_full[st]);
+      load(p.k_codes, grow1, kw);
+      ok = i < NST || mbar_wait(&v_free[st], ph, p.err, (const volatile int*)s_abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        *s_abort = 1;
+        break;
+      }
+      // pages with V scale 0 count as zeros, whatever their codes
+      const uint32_t zero = __ballot_sync(0xffffffffu, grow >= 0 && !(vs > 0.f));
+      if (zero) {
+#pragma unroll
+        for (int x = 0; x < PER; ++x)
+          if (zero >> ((x * Cfg::RPP + rr) >> 4) & 1u) vw[x] = make_uint4(0u, 0u, 0u, 0u);
+      }
+      store(v_s + st * Cfg::KTILE, vw);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&v_full[st]);
+      load(p.v_codes, grow1, vw);
+      grow = grow1;
+      scales(grow);
+      grow1 = group_row(i + 2);
+    }
+  } else if (lane == 0) {
+    // ================================================================== MMA issuer
+    constexpr uint32_t idS = idesc_f16_f32(128, KT, false);
+    constexpr uint32_t idO = idesc_f16_f32(128, HD, true);
+    const uint32_t qa = smem_u32(q_s), ka = smem_u32(k_s), va = smem_u32(v_s);
+    auto issue_s = [&](int i, int j, int sb) {
+      const uint32_t kb = ka + (i % NST) * Cfg::KTILE, qb = qa + j * Cfg::QTILE;
+#pragma unroll
+      for (int kk = 0; kk < HD / 16; ++kk)
+        tc_mma_f16(tmem + sb * Cfg::S_COLS, smem_desc_sw128(qb + (kk >> 2) * Cfg::QBOX + (kk & 3) * 32),
+                   smem_desc_sw128(kb + (kk >> 2) * Cfg::KBOX + (kk & 3) * 32), idS, kk != 0);
+      tc_commit(&s_full[sb]);
+    };
+    auto issue_pv = [&](int i, int j, int sb) {
+      const uint32_t vb = va + (i % NST) * Cfg::KTILE;
+#pragma unroll
+      for (int kk = 0; kk < KT / 16; ++kk)
+        tc_mma_f16_ts(tmem + Cfg::O_COL + j * HD, tmem + sb * Cfg::S_COLS + kk * 8,
+                      smem_desc_sw128_mn(vb + kk * 2048, Cfg::KBOX), idO, (i | kk) != 0);
+    };
+    const volatile int* ab = (const volatile int*)s_abort;
+    bool ok = mbar_wait(q_full, 0, p.err, ab);
+    if (QT == 2) {
+      // tile i: P V of tile i - 1, then S of tile i, for each row tile in turn
+      for (int i = 0; ok && i <= nt; ++i) {
+        if (i < nt) ok = mbar_wait(&k_full[i % NST], (i / NST) & 1, p.err, ab);
+        if (ok && i > 0) ok = mbar_wait(&v_full[(i - 1) % NST], ((i - 1) / NST) & 1, p.err, ab);
+        for (int j = 0; ok && j < tiles; ++j) {
+          if (i > 0) {
+            ok = mbar_wait(&p_full[j], (i - 1) & 1, p.err, ab);
+            if (!ok) break;
+            tc_fence_after();
+            issue_pv(i - 1, j, j);
+            if (i == nt) tc_commit(&o_full[j]);
+          }
+          tc_fence_after();
+          if (i < nt) issue_s(i, j, j);
+        }
+        if (!ok) break;
+        if (i > 0) tc_commit(&v_free[(i - 1) % NST]);
+        if (i < nt) tc_commit(&k_free[i % NST]);
+      }
+    } else {
+      // S of tile i + 1 runs while tile i is in its softmax
+      for (int i = -1; ok && i < nt; ++i) {
+        if (i + 1 < nt) {
+          ok = mbar_wait(&k_full[(i + 1) % NST], ((i + 1) / NST) & 1, p.err, ab);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(i + 1, 0, (i + 1) & 1);
+          tc_commit(&k_free[(i + 1) % NST]);
+        }
+        if (i >= 0) {
+          ok = mbar_wait(&v_full[i % NST], (i / NST) & 1, p.err, ab) &&
+               mbar_wait(&p_full[i & 1], (i >> 1) & 1, p.err, ab);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(i, 0, i & 1);
+          tc_commit(pv_done);
+          if (i == nt - 1) tc_commit(&o_full[0]);
+          tc_commit(&v_free[i % NST]);
+        }
+      }
+    }
+    if (!ok) {
+      // what was issued finishes before the tensor memory goes
+      *s_abort = 1;
+      tc_commit(drain);
+      mbar_wait(drain, 0, p.err);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+// Adds the parts of items shared by several CTAs: a warp per row.
+template <int HD>
+__global__ void __launch_bounds__(256) paged_block_merge_kernel(const PagedAttnArgs a, int splits) {
+  using Cfg = BlockCfg<HD>;
+  constexpr int RS = kPagedRecord(HD);
+  const PagedView& p = a.p;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.nh / p.nkv;
+  pdl_wait();
+  BlockItem it;
+  const int u = blockIdx.x / (Cfg::ROWS / 8);
+  if (!block_item<HD>(a, splits, u * splits, &it)) return;
+  const int r = (blockIdx.x % (Cfg::ROWS / 8)) * 8 + warp;
+  if (r >= it.rows) return;
+  const float* rec = a.block_records + ((size_t)u * splits * Cfg::ROWS + r) * RS;
+  const size_t step = (size_t)Cfg::ROWS * RS;
+  float M = kNoMax, my_m = kNoMax, my_l = 0.f;
+  if (lane < splits) {
+    const float2 y = __ldcg(reinterpret_cast<const float2*>(rec + lane * step + HD));
+    my_m = y.x;
+    my_l = y.y;
+  }
+  M = my_m;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  float f = my_l > 0.f ? exp2f(my_m - M) : 0.f;
+  const float l = warp_sum(f * my_l);
+  f = l > 0.f ? f / l : 0.f;
+  const int R = it.r0 + r, tok = R / G;
+  constexpr int Q = (HD + 127) / 128;
+  float4 acc[Q];
+#pragma unroll
+  for (int q = 0; q < Q; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < splits; ++s) {
+    const float w = __shfl_sync(0xffffffffu, f, s);
+    if (w == 0.f) continue;  // a part without visible keys wrote no O
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      const int d = 4 * (lane + 32 * q);
+      if (d < HD) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(rec + s * step + d));
+        acc[q].x += w * v.x, acc[q].y += w * v.y, acc[q].z += w * v.z, acc[q].w += w * v.w;
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    const int d = 4 * (lane + 32 * q);
+    if (d < HD) paged_store_o4(a, it.row0 + tok, it.kvh * G + R - tok * G, d, acc[q]);
+  }
+}
+
+template <int HD>
+cudaError_t launch_block_hd(const PagedAttnArgs& a, int slots, int splits, cudaStream_t s) {
+  using Cfg = BlockCfg<HD>;
+  cudaError_t e = cudaFuncSetAttribute(paged_block_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+  const int units = slots * a.p.nkv;
+  paged_block_kernel<HD><<<units * splits, Cfg::THREADS, Cfg::SMEM, s>>>(a, splits);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || splits == 1) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * (Cfg::ROWS / 8)));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_block_merge_kernel<HD>, a, splits);
+}
+
+}  // namespace
+
+int paged_block_rows(int hd) { return hd == 256 ? BlockCfg<256>::ROWS : BlockCfg<128>::ROWS; }
+int paged_block_keys(int hd) { return hd == 256 ? BlockCfg<256>::KT : BlockCfg<128>::KT; }
+
+cudaError_t launch_paged_block(const PagedAttnArgs& a, int slots, int splits, cudaStream_t s) {
+  if (a.p.hd == 64) return launch_block_hd<64>(a, slots, splits, s);
+  if (a.p.hd == 128) return launch_block_hd<128>(a, slots, splits, s);
+  return launch_block_hd<256>(a, slots, splits, s);
+}
+
+}  // namespace hfa
