@@ -562,8 +562,8 @@ class Pages:
             if table_host.shape != tuple(table.shape):
                 raise HfaError(HFA_EINVAL, "table and table_host have different shapes")
         self.tensors = (k_codes, k_scales, v_codes, v_scales, table, table_host)
-        self.batch, self.max_pages = table.shape
-        self.shape = tuple(k_codes.shape)
+        self.batch, max_pages = table.shape
+        self.shape = (*k_codes.shape, max_pages)  # what a descriptor has to agree with
         self.c = hfa_pages(k_codes.data_ptr(), k_scales.data_ptr(), v_codes.data_ptr(),
                            v_scales.data_ptr(), table.data_ptr(),
                            None if table_host is None else table_host.ctypes.data)
@@ -592,59 +592,58 @@ class Paged:
                                     _stream_ptr(stream), ctypes.byref(self._h))
         if st != HFA_OK:
             raise HfaError(st, lib().hfa_paged_last_error(None).decode())
-        self._pool = (desc.num_pages, desc.num_kv_heads, desc.page_size, desc.head_dim)
+        self._shape = (desc.num_pages, desc.num_kv_heads, desc.page_size, desc.head_dim, desc.max_pages)
+        self._nh, self._nkv, self._hd = desc.num_heads, desc.num_kv_heads, desc.head_dim
 
     def _check(self, st: int):
         if st != HFA_OK:
             raise HfaError(st, lib().hfa_paged_last_error(self._h).decode())
 
-    def _batch(self, ints, pages: Pages) -> list:
-        """Host int32 arrays of a call; the pool and the table fit the descriptor."""
-        if pages.shape != self._pool or pages.max_pages != self.desc.max_pages:
-            raise HfaError(HFA_EINVAL, f"a pool {pages.shape} with {pages.max_pages} table entries, "
-                                       f"the cache is {self._pool} with {self.desc.max_pages}")
-        return [np.ascontiguousarray(x, dtype=np.int32) for x in ints]
+    def _pages(self, pages: Pages, batch: int) -> None:
+        if pages.shape != self._shape:
+            raise HfaError(HFA_EINVAL, f"a pool and table {pages.shape}, the cache is {self._shape}")
+        if pages.batch < batch or batch < 1:
+            raise HfaError(HFA_EINVAL, f"{batch} sequences, the table has {pages.batch}")
 
-    def _rows(self, x: torch.Tensor, heads: int, total: int, dtype=None):
+    def _rows(self, x: torch.Tensor, heads: int, total: int, dtype) -> tuple:
         """(data pointer, row stride) of a [total, heads, hd] array whose heads are dense."""
-        hd = self.desc.head_dim
-        if x.shape != (total, heads, hd) or (dtype is not None and x.dtype != dtype):
+        hd = self._hd
+        if x.shape != (total, heads, hd) or x.dtype is not dtype:
             raise HfaError(HFA_EINVAL, f"rows {tuple(x.shape)} {x.dtype}, expected "
-                                       f"{(total, heads, hd)} {dtype or ''}")
-        st = x.stride()
-        if total and (st[2] != 1 or (heads > 1 and st[1] != hd)):
+                                       f"{(total, heads, hd)} {dtype}")
+        s0, s1, s2 = x.stride()
+        if total and (s2 != 1 or (s1 != hd and heads > 1)):
             raise HfaError(HFA_EINVAL, "the heads of a row must be dense")
-        return x.data_ptr(), st[0] if total > 1 else heads * hd
+        return x.data_ptr(), s0 if total > 1 else heads * hd
 
-    @staticmethod
-    def _dtype(x: torch.Tensor) -> int:
-        if x.dtype == torch.bfloat16:
-            return HFA_BF16
-        if x.dtype == torch.float32:
-            return HFA_F32
-        raise HfaError(HFA_EINVAL, f"rows of {x.dtype}: bf16 or f32")
+    def _dense(self, x: torch.Tensor, total: int, dtype) -> int:
+        ptr, stride = self._rows(x, self._nh, total, dtype)
+        if stride != self._nh * self._hd:
+            raise HfaError(HFA_EINVAL, "the output rows must be dense")
+        return ptr
 
     def hfa_paged_append(self, cu_dev: torch.Tensor, cu_host, start_dev: torch.Tensor, start_host,
                          q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pages: Pages,
                          q_out: Optional[torch.Tensor] = None, stream=None) -> None:
-        cu, start = self._batch((cu_host, start_host), pages)
-        batch, total = _ragged(cu, start, pages, cu_dev, start_dev)
-        dtype = self._dtype(k)
-        nh, nkv = self.desc.num_heads, self.desc.num_kv_heads
-        kp, ks = self._rows(k, nkv, total)
-        vp, vs = self._rows(v, nkv, total, k.dtype)
+        cu, cup = _ints(cu_host, cu_dev)
+        start, startp = _ints(start_host, start_dev)
+        batch = start.size
+        self._pages(pages, batch)
+        total = _total(cu, batch)
+        kind = k.dtype
+        kp, ks = self._rows(k, self._nkv, total, kind)
+        vp, vs = self._rows(v, self._nkv, total, kind)
         qp, qs, op = None, 0, None
         if q is not None:
             if q_out is None:
                 raise HfaError(HFA_EINVAL, "queries without q_out")
-            qp, qs = self._rows(q, nh, total, k.dtype)
-            op, os_ = self._rows(q_out, nh, total, k.dtype)
-            if os_ != nh * self.desc.head_dim:
-                raise HfaError(HFA_EINVAL, "q_out must be dense")
-        st = lib().hfa_paged_append(self._h, _stream_ptr(stream), batch, cu_dev.data_ptr(),
-                                    cu.ctypes.data, start_dev.data_ptr(), start.ctypes.data, qp, qs,
-                                    kp, ks, vp, vs, dtype, pages.ref, op)
-        self._check(st)
+            qp, qs = self._rows(q, self._nh, total, kind)
+            op = self._dense(q_out, total, kind)
+        st = lib().hfa_paged_append(self._h, _stream_handle(stream), batch, cu_dev.data_ptr(), cup,
+                                    start_dev.data_ptr(), startp, qp, qs, kp, ks, vp, vs,
+                                    _row_type(kind), pages.ref, op)
+        if st:
+            self._check(st)
 
     def hfa_paged_workspace_bytes(self, batch: int, total_rows: int) -> int:
         return int(lib().hfa_paged_workspace_bytes(self._h, int(batch), int(total_rows)))
@@ -652,36 +651,40 @@ class Paged:
     def hfa_paged_attention(self, cu_dev: torch.Tensor, cu_host, len_dev: torch.Tensor, len_host,
                             q: torch.Tensor, pages: Pages, workspace: torch.Tensor, o: torch.Tensor,
                             stream=None) -> torch.Tensor:
-        cu, lens = self._batch((cu_host, len_host), pages)
-        batch, total = _ragged(cu, lens, pages, cu_dev, len_dev)
-        nh = self.desc.num_heads
-        qp, qs = self._rows(q, nh, total)
-        op, os_ = self._rows(o, nh, total, q.dtype)
-        if os_ != nh * self.desc.head_dim:
-            raise HfaError(HFA_EINVAL, "o must be dense")
-        st = lib().hfa_paged_attention(self._h, _stream_ptr(stream), batch, cu_dev.data_ptr(),
-                                       cu.ctypes.data, len_dev.data_ptr(), lens.ctypes.data, qp, qs,
-                                       self._dtype(q), pages.ref, workspace.data_ptr(),
-                                       workspace.numel() * workspace.element_size(), op)
-        self._check(st)
+        cu, cup = _ints(cu_host, cu_dev)
+        lens, lenp = _ints(len_host, len_dev)
+        batch = lens.size
+        self._pages(pages, batch)
+        total = _total(cu, batch)
+        qp, qs = self._rows(q, self._nh, total, q.dtype)
+        op = self._dense(o, total, q.dtype)
+        st = lib().hfa_paged_attention(self._h, _stream_handle(stream), batch, cu_dev.data_ptr(), cup,
+                                       len_dev.data_ptr(), lenp, qp, qs, _row_type(q.dtype),
+                                       pages.ref, workspace.data_ptr(), workspace.nbytes, op)
+        if st:
+            self._check(st)
         return o
 
     def hfa_paged_read(self, start_dev: torch.Tensor, start_host, count_dev: torch.Tensor, count_host,
                        pages: Pages, k_cache: torch.Tensor, v_cache: torch.Tensor, stream=None) -> None:
-        start, count = self._batch((start_host, count_host), pages)
+        start, startp = _ints(start_host, start_dev)
+        count, countp = _ints(count_host, count_dev)
         batch = start.size
-        if count.size != batch or pages.batch < batch or start_dev.numel() < batch or \
-                count_dev.numel() < batch or start_dev.dtype != torch.int32 or \
-                count_dev.dtype != torch.int32:
-            raise HfaError(HFA_EINVAL, "start, count and the table do not agree on the batch")
-        want = (batch, self.desc.num_kv_heads, k_cache.shape[2], self.desc.head_dim)
+        self._pages(pages, batch)
+        if count.size != batch:
+            raise HfaError(HFA_EINVAL, f"{batch} starts, {count.size} counts")
+        shape = k_cache.shape
+        if len(shape) != 4 or shape[0] != batch or shape[1] != self._nkv or shape[3] != self._hd or \
+                v_cache.shape != shape:
+            raise HfaError(HFA_EINVAL, f"the caches are [{batch}, {self._nkv}, capacity, {self._hd}]")
         for c in (k_cache, v_cache):
-            if tuple(c.shape) != want or c.dtype != torch.bfloat16 or not c.is_contiguous():
-                raise HfaError(HFA_EINVAL, f"the caches are contiguous bf16 {want}")
-        self._check(lib().hfa_paged_read(self._h, _stream_ptr(stream), batch, start_dev.data_ptr(),
-                                         start.ctypes.data, count_dev.data_ptr(), count.ctypes.data,
-                                         pages.ref, int(k_cache.shape[2]), k_cache.data_ptr(),
-                                         v_cache.data_ptr()))
+            if c.dtype is not torch.bfloat16 or not c.is_contiguous():
+                raise HfaError(HFA_EINVAL, "the caches must be contiguous bf16")
+        st = lib().hfa_paged_read(self._h, _stream_handle(stream), batch, start_dev.data_ptr(), startp,
+                                  count_dev.data_ptr(), countp, pages.ref, shape[2],
+                                  k_cache.data_ptr(), v_cache.data_ptr())
+        if st:
+            self._check(st)
 
     def hfa_paged_check_status(self, stream=None) -> None:
         self._check(lib().hfa_paged_check_status(self._h, _stream_ptr(stream)))
@@ -698,11 +701,32 @@ class Paged:
             pass
 
 
-def _ragged(cu: np.ndarray, per: np.ndarray, pages: Pages, cu_dev: torch.Tensor,
-            per_dev: torch.Tensor):
-    """(batch, rows) of a ragged call, its arrays agreeing on the batch."""
-    batch = per.size
-    if batch < 1 or cu.size != batch + 1 or pages.batch < batch or cu_dev.numel() < batch + 1 or \
-            per_dev.numel() < batch or cu_dev.dtype != torch.int32 or per_dev.dtype != torch.int32:
-        raise HfaError(HFA_EINVAL, "cu, the lengths and the table do not agree on the batch")
-    return batch, int(cu[-1])
+def _ints(host, dev: torch.Tensor) -> tuple:
+    """(host int32 array, its address) of one per-sequence argument and its device copy."""
+    a = np.ascontiguousarray(host, dtype=np.int32)
+    if dev.dtype is not torch.int32 or dev.numel() < a.size or not dev.is_contiguous():
+        raise HfaError(HFA_EINVAL, f"the device copy of {a.size} integers: {dev.numel()} of {dev.dtype}")
+    if a.size == 0 or not a.flags.writeable:  # from_buffer takes neither
+        return a, a.ctypes.data
+    return a, ctypes.addressof(ctypes.c_char.from_buffer(a))
+
+
+def _total(cu: np.ndarray, batch: int) -> int:
+    if cu.size != batch + 1:
+        raise HfaError(HFA_EINVAL, f"cu has {cu.size} entries for {batch} sequences")
+    return cu.item(-1)
+
+
+def _row_type(dtype) -> int:
+    if dtype is torch.bfloat16:
+        return HFA_BF16
+    if dtype is torch.float32:
+        return HFA_F32
+    raise HfaError(HFA_EINVAL, f"rows of {dtype}: bf16 or f32")
+
+
+def _stream_handle(stream) -> int:
+    """The stream's handle; the current stream's without building a Stream object."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
