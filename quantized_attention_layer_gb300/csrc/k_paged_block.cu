@@ -168,7 +168,7 @@ __device__ __forceinline__ bool block_item(const PagedAttnArgs& a, int splits, i
   return true;
 }
 
-template <int HD>
+template <int HD, bool CAP>
 __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     paged_block_kernel(const PagedAttnArgs a, int splits) {
   using Cfg = BlockCfg<HD>;
@@ -327,32 +327,42 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       const float* lvs = s_lvs + sc * NG;
       const float* ivs = s_ivs + sc * NG;
       const bool masked = key0 < wlo || key0 + KT > whi || s_flag[sc];
-      // ---- maximum of s + log2 vs
+      // ---- maximum of s + log2 vs (the loops stay rolled: unrolled, the three roles' code
+      // outgrows the instruction caches and the softmax takes three times as long)
       float top = -INFINITY;
+      auto raise = [&](int gr, float gm) {
+        float s = gm * (ks[gr] * rowf);
+        if (CAP) s = a.cap_log2 * tanh_ex2(s);
+        top = fmaxf(top, s + lvs[gr]);
+      };
+      if (!masked) {
+#pragma unroll 1
+        for (int c = 0; c < NG; c += 4) {
+          uint32_t x[4][16];
 #pragma unroll
-      for (int c = 0; c < NG / 2; ++c) {
-        uint32_t x[2][16];
-        tmem_ld16_nowait(t_s + 32 * c, x[0]);
-        tmem_ld16_nowait(t_s + 32 * c + 16, x[1]);
-        tmem_wait_ld();
+          for (int h = 0; h < 4; ++h) tmem_ld16_nowait(t_s + 16 * (c + h), x[h]);
+          tmem_wait_ld();
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int gr = 2 * c + h;
+          for (int h = 0; h < 4; ++h) {
+            float gm = __uint_as_float(x[h][0]);
+#pragma unroll
+            for (int e = 1; e < 16; ++e) gm = fmaxf(gm, __uint_as_float(x[h][e]));
+            raise(c + h, gm);
+          }
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < NG; ++c) {
+          uint32_t x[16];
+          tmem_ld16_nowait(t_s + 16 * c, x);
+          tmem_wait_ld();
+          // this row's keys of the group: columns [from, to)
+          const int from = lim.x - (key0 + 16 * c), to = ks[c] >= 0.f ? lim.y - (key0 + 16 * c) : 0;
           float gm = -INFINITY;
-          if (!masked) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) gm = fmaxf(gm, __uint_as_float(x[h][e]));
-          } else if (ks[gr] >= 0.f) {
-            const int k0 = key0 + 16 * gr;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (k0 + e >= lim.x && k0 + e < lim.y) gm = fmaxf(gm, __uint_as_float(x[h][e]));
-          }
-          if (gm != -INFINITY) {
-            float s = gm * (ks[gr] * rowf);
-            if (a.cap_log2 != 0.f) s = a.cap_log2 * tanh_ex2(s);
-            top = fmaxf(top, s + lvs[gr]);
-          }
+          for (int e = 0; e < 16; ++e)
+            if (e >= from && e < to) gm = fmaxf(gm, __uint_as_float(x[e]));
+          if (gm != -INFINITY) raise(c, gm);
         }
       }
       // ---- the maximum moves: O follows
@@ -382,42 +392,55 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
           tmem_wait_st();
         }
       }
-      // ---- weights, over the scores' own columns
+      // ---- weights, over the scores' own columns: group c's 16 scores become 8 words
+      auto weights = [&](int c, const uint32_t (&x)[16], uint32_t* w, int from, int to) {
+        const float kq = ks[c] * rowf, sh = lvs[c] - mw;
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-      for (int c = 0; c < NG / 2; ++c) {
-        uint32_t x[2][16], w[16];
-        tmem_ld16_nowait(t_s + 32 * c, x[0]);
-        tmem_ld16_nowait(t_s + 32 * c + 16, x[1]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int gr = 2 * c + h;
-          const float kq = ks[gr] * rowf, sh = lvs[gr] - mw;
-          float2 sum = make_float2(0.f, 0.f);
-          const int k0 = key0 + 16 * gr;
-          const bool none = masked && ks[gr] < 0.f;
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float2 s = make_float2(__uint_as_float(x[h][e]), __uint_as_float(x[h][e + 1]));
-            if (a.cap_log2 == 0.f) {
-              s = fma2(s, make_float2(kq, kq), make_float2(sh, sh));
-            } else {
-              s = mul2(s, make_float2(kq, kq));
-              s.x = a.cap_log2 * tanh_ex2(s.x) + sh;
-              s.y = a.cap_log2 * tanh_ex2(s.y) + sh;
-            }
-            s.x = ex2_approx(s.x);
-            s.y = ex2_approx(s.y);
-            if (masked) {
-              if (none || k0 + e < lim.x || k0 + e >= lim.y) s.x = 0.f;
-              if (none || k0 + e + 1 < lim.x || k0 + e + 1 >= lim.y) s.y = 0.f;
-            }
-            sum = add2(sum, s);
-            w[8 * h + (e >> 1)] = pack_h2(__float2half_rn(s.x), __float2half_rn(s.y));
+        for (int e = 0; e < 16; e += 2) {
+          float2 s = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+          if (!CAP) {
+            s = fma2(s, make_float2(kq, kq), make_float2(sh, sh));
+          } else {
+            s = mul2(s, make_float2(kq, kq));
+            s.x = a.cap_log2 * tanh_ex2(s.x) + sh;
+            s.y = a.cap_log2 * tanh_ex2(s.y) + sh;
           }
-          l += (sum.x + sum.y) * ivs[gr];
+          s.x = ex2_approx(s.x);
+          s.y = ex2_approx(s.y);
+          if (e < from || e >= to) s.x = 0.f;
+          if (e + 1 < from || e + 1 >= to) s.y = 0.f;
+          sum = add2(sum, s);
+          w[e >> 1] = pack_h2(__float2half_rn(s.x), __float2half_rn(s.y));
         }
-        tmem_st16(t_s + 16 * c, w);
+        l += (sum.x + sum.y) * ivs[c];
+      };
+      if (!masked) {
+#pragma unroll 1
+        for (int c = 0; c < NG; c += 4) {
+          uint32_t x[4][16], w[2][16];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) tmem_ld16_nowait(t_s + 16 * (c + h), x[h]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int h = 0; h < 4; ++h) weights(c + h, x[h], w[h >> 1] + 8 * (h & 1), 0, 16);
+          tmem_st16(t_s + 8 * c, w[0]);
+          tmem_st16(t_s + 8 * c + 16, w[1]);
+        }
+      } else {
+#pragma unroll 1
+        for (int c = 0; c < NG; c += 2) {
+          uint32_t x[2][16], w[16];
+          tmem_ld16_nowait(t_s + 16 * c, x[0]);
+          tmem_ld16_nowait(t_s + 16 * c + 16, x[1]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int k0 = key0 + 16 * (c + h);
+            weights(c + h, x[h], w + 8 * h, lim.x - k0, ks[c + h] >= 0.f ? lim.y - k0 : 0);
+          }
+          tmem_st16(t_s + 8 * c, w);
+        }
       }
       tmem_wait_st();
       tc_fence_before();
@@ -713,10 +736,11 @@ __global__ void __launch_bounds__(256) paged_block_merge_kernel(const PagedAttnA
 template <int HD>
 cudaError_t launch_block_hd(const PagedAttnArgs& a, int slots, int splits, cudaStream_t s) {
   using Cfg = BlockCfg<HD>;
-  cudaError_t e = cudaFuncSetAttribute(paged_block_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
+  auto kern = a.cap_log2 != 0.f ? paged_block_kernel<HD, true> : paged_block_kernel<HD, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
   if (e != cudaSuccess) return e;
   const int units = slots * a.p.nkv;
-  paged_block_kernel<HD><<<units * splits, Cfg::THREADS, Cfg::SMEM, s>>>(a, splits);
+  kern<<<units * splits, Cfg::THREADS, Cfg::SMEM, s>>>(a, splits);
   e = cudaGetLastError();
   if (e != cudaSuccess || splits == 1) return e;
   cudaLaunchConfig_t cfg = {};
