@@ -91,6 +91,22 @@ cudaError_t launch_paged_step(const PagedAttnArgs& a, const CUtensorMap& tk, con
 
 // ------------------------------------------------------------------ device helpers
 #ifdef __CUDACC__
+// mbar_wait with its limit in SM cycles (about 2 s): between two tries it reads the cycle
+// counter, a few cycles, where the nanosecond timer takes long enough to delay every hand-over
+// of a pipeline that waits on each tile
+constexpr long long kPagedWaitCycles = 4000000000ll;
+__device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, unsigned* err,
+                                           const volatile int* abort = nullptr) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (abort && *abort) return false;
+    if (clock64() - t0 > kPagedWaitCycles) break;
+  }
+  atomicOr(err, kErrWaitTimeout);
+  return false;
+}
 // four adjacent dims of an output row
 __device__ __forceinline__ void paged_store_o4(const PagedAttnArgs& a, int row, int h, int d, float4 v) {
   const size_t at = ((size_t)row * a.p.nh + h) * a.p.hd + d;

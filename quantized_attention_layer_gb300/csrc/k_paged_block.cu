@@ -43,9 +43,9 @@ struct BlockCfg {
   static constexpr int ROWS = QT * 128;
   static constexpr int KT = HD == 256 ? 64 : 128; // keys of a tile
   static constexpr int NG = KT / 16;              // 16-key groups: one scale each
-  static constexpr int NCW = HD == 256 ? 8 : 4;   // converter warps
   static constexpr int SMW = QT * 4;              // softmax warps
-  static constexpr int THREADS = (SMW + NCW + 1) * 32;
+  static constexpr int NCW = 15 - SMW;            // converter warps; warp 15 issues the MMAs
+  static constexpr int THREADS = 512;
   static constexpr int BOXES = HD / 64;
   static constexpr int QBOX = 128 * 128;          // bytes of a 64-dim box of a row tile
   static constexpr int QTILE = BOXES * QBOX;
@@ -54,14 +54,15 @@ struct BlockCfg {
   static constexpr int NST = 2;                   // operand stages of K and of V
   static constexpr int NSC = 4;                   // scale slots (see sc_full)
   static constexpr int SMEM_OPS = QT * QTILE + 2 * NST * KTILE;
-  static constexpr size_t SMEM = 1024 + SMEM_OPS + ROWS * 4 + NSC * (NG * 12 + 16) + 256;
+  static constexpr size_t SMEM = 1024 + SMEM_OPS + ROWS * 4 + NSC * (NG * 16 + 16) + 256;
   static constexpr int S_COLS = KT;
   static constexpr int O_COL = 2 * KT;            // TMEM: S buffers, then O tiles
-  static constexpr int PER = KT * HD / 16 / (NCW * 32);  // 16-byte loads of a converter thread
-  static constexpr int CPR = HD / 16;                    // 16-byte chunks of a row
-  static constexpr int RPP = NCW * 32 / CPR;             // rows of one pass of the converters
+  static constexpr int CPR = HD / 16;             // 16-byte chunks of a row of codes
+  static constexpr int RPU = 32 / CPR;            // rows of a converter's unit: 32 chunks
+  static constexpr int NU = KT / RPU;             // units of a tile
+  static constexpr int PER = (NU + NCW - 1) / NCW;  // units of one warp
   static_assert(O_COL + QT * HD <= 512, "TMEM");
-  static_assert(RPP % 16 == 0 || 16 % RPP == 0, "a pass covers whole groups, or lies in one");
+  static_assert(16 % RPU == 0, "a unit lies in one group");
   static_assert(SMEM <= 232448, "shared memory");
 };
 
@@ -105,6 +106,21 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
+}
+__device__ __forceinline__ uint32_t cvt_h2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// tmem_st16 that other memory accesses may move across: its order against the reads of the
+// same columns is that of the volatile statements
+__device__ __forceinline__ void tmem_st16_free(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]));
 }
 // tanh to about 1e-7 absolute from one exponential and one reciprocal
 __device__ __forceinline__ float tanh_ex2(float x) {
@@ -172,17 +188,16 @@ template <int HD, bool CAP>
 __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     paged_block_kernel(const PagedAttnArgs a, int splits) {
   using Cfg = BlockCfg<HD>;
-  constexpr int QT = Cfg::QT, KT = Cfg::KT, NG = Cfg::NG, NST = Cfg::NST, NSC = Cfg::NSC;
+  constexpr int QT = Cfg::QT, KT = Cfg::KT, NG = Cfg::NG, HG = NG / 2, NST = Cfg::NST, NSC = Cfg::NSC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_align1024(smem_raw);
   uint8_t* q_s = smem;
   uint8_t* k_s = smem + QT * Cfg::QTILE;
   uint8_t* v_s = k_s + NST * Cfg::KTILE;
   float* s_rowf = reinterpret_cast<float*>(smem + Cfg::SMEM_OPS);  // [ROWS] qscale 2^e
-  float* s_ks = s_rowf + Cfg::ROWS;   // [NSC][NG] K scale, -1: the group is not visible
-  float* s_lvs = s_ks + NSC * NG;     // log2 of the V scale
-  float* s_ivs = s_lvs + NSC * NG;    // 1 / 2^(that)
-  int* s_flag = reinterpret_cast<int*>(s_ivs + NSC * NG);  // [NSC] some group is refused
+  // [NSC][NG] K scale (-1: the group is not visible), log2 of the V scale, 1 / the V scale
+  float4* s_sc = reinterpret_cast<float4*>(s_rowf + Cfg::ROWS);
+  int* s_flag = reinterpret_cast<int*>(s_sc + NSC * NG);  // [NSC] some group is refused
   uint64_t* bars = reinterpret_cast<uint64_t*>(s_flag + NSC);
   uint64_t* q_full = bars;            // 1
   uint64_t* k_full = bars + 1;        // [NST] converted K tiles
@@ -193,10 +208,11 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
                                       // tile t + NSC - NST's S is done, hence after every
                                       // softmax of tile t
   uint64_t* s_full = sc_full + NSC;   // [2] S ready
-  uint64_t* p_full = s_full + 2;      // [2] P written
-  uint64_t* o_full = p_full + 2;      // [2] a row tile's last O += P V is complete
-  uint64_t* pv_done = o_full + 2;     // QT 1: each tile's O += P V is complete
-  uint64_t* drain = pv_done + 1;      // after an abort: what was issued is complete
+  uint64_t* p_full = s_full + 2;      // [2][2] each half of P written
+  uint64_t* o_full = p_full + 4;      // [2] a row tile's last O += P V is complete
+  uint64_t* pv_half = o_full + 2;     // [2] O += P V of each tile's first half is complete,
+  uint64_t* pv_done = pv_half + 2;    // [2] of the whole tile
+  uint64_t* drain = pv_done + 2;      // after an abort: what was issued is complete
   volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1) + 1;
   BlockItem* s_item = reinterpret_cast<BlockItem*>(s_tmem + 1);
@@ -223,10 +239,12 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       for (int i = 0; i < NSC; ++i) mbar_init(&sc_full[i], 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(&s_full[i], 1);
-        mbar_init(&p_full[i], 4);
+        mbar_init(&p_full[2 * i], 4);
+        mbar_init(&p_full[2 * i + 1], 4);
         mbar_init(&o_full[i], 1);
+        mbar_init(&pv_half[i], 1);
+        mbar_init(&pv_done[i], 1);
       }
-      mbar_init(pv_done, 1);
       mbar_init(drain, 1);
       *s_abort = 0;
       fence_barrier_init();
@@ -315,141 +333,133 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       const int key0 = (it.t0 + i) * KT;
       const uint32_t t_s = t_lane + sb * Cfg::S_COLS;
       const uint32_t t_o = t_lane + Cfg::O_COL + j * HD;
-      ok = mbar_wait(&sc_full[sc], (i / NSC) & 1, p.err, (const volatile int*)s_abort) &&
-           mbar_wait(&s_full[sb], ph, p.err, (const volatile int*)s_abort);
+      ok = paged_wait(&sc_full[sc], (i / NSC) & 1, p.err, (const volatile int*)s_abort) &&
+           paged_wait(&s_full[sb], ph, p.err, (const volatile int*)s_abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
         *s_abort = 1;
         break;
       }
       tc_fence_after();
-      const float* ks = s_ks + sc * NG;
-      const float* lvs = s_lvs + sc * NG;
-      const float* ivs = s_ivs + sc * NG;
+      const float4* scale = s_sc + sc * NG;
       const bool masked = key0 < wlo || key0 + KT > whi || s_flag[sc];
-      // ---- maximum of s + log2 vs (the loops stay rolled: unrolled, the three roles' code
-      // outgrows the instruction caches and the softmax takes three times as long)
-      float top = -INFINITY;
-      auto raise = [&](int gr, float gm) {
-        float s = gm * (ks[gr] * rowf);
-        if (CAP) s = a.cap_log2 * tanh_ex2(s);
-        top = fmaxf(top, s + lvs[gr]);
-      };
-      if (!masked) {
+      // two halves of the tile's keys, each with its own look at the maximum: half the scores
+      // in registers, and the MMA starts on the first half while the second is formed
 #pragma unroll 1
-        for (int c = 0; c < NG; c += 4) {
-          uint32_t x[4][16];
+      for (int half = 0; half < 2; ++half) {
+        const uint32_t t_h = t_s + half * (KT / 2);
+        const float4* f4 = scale + half * HG;
+        const int kh = key0 + half * (KT / 2);
+        uint32_t x[HG][16];
 #pragma unroll
-          for (int h = 0; h < 4; ++h) tmem_ld16_nowait(t_s + 16 * (c + h), x[h]);
-          tmem_wait_ld();
+        for (int c = 0; c < HG; ++c) tmem_ld16_nowait(t_h + 16 * c, x[c]);
+        tmem_wait_ld();
+        // ---- maximum of s + log2 vs
+        float top = -INFINITY;
+        auto raise = [&](int gr, float gm) {
+          const float4 f = f4[gr];
+          float s = gm * (f.x * rowf);
+          if (CAP) s = a.cap_log2 * tanh_ex2(s);
+          top = fmaxf(top, s + f.y);
+        };
+        if (!masked) {
 #pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            float gm = __uint_as_float(x[h][0]);
+          for (int c = 0; c < HG; ++c) {
+            float gm = __uint_as_float(x[c][0]);
 #pragma unroll
-            for (int e = 1; e < 16; ++e) gm = fmaxf(gm, __uint_as_float(x[h][e]));
-            raise(c + h, gm);
+            for (int e = 1; e < 16; ++e) gm = fmaxf(gm, __uint_as_float(x[c][e]));
+            raise(c, gm);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < HG; ++c) {
+            // this row's keys of the group: columns [from, to)
+            const int from = lim.x - (kh + 16 * c), to = f4[c].x >= 0.f ? lim.y - (kh + 16 * c) : 0;
+            float gm = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e >= from && e < to) gm = fmaxf(gm, __uint_as_float(x[c][e]));
+            if (gm != -INFINITY) raise(c, gm);
           }
         }
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < NG; ++c) {
-          uint32_t x[16];
-          tmem_ld16_nowait(t_s + 16 * c, x);
-          tmem_wait_ld();
-          // this row's keys of the group: columns [from, to)
-          const int from = lim.x - (key0 + 16 * c), to = ks[c] >= 0.f ? lim.y - (key0 + 16 * c) : 0;
-          float gm = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (e >= from && e < to) gm = fmaxf(gm, __uint_as_float(x[e]));
-          if (gm != -INFINITY) raise(c, gm);
-        }
-      }
-      // ---- the maximum moves: O follows
-      if (__any_sync(0xffffffffu, top > mw + kLazy)) {
-        const float mn = fmaxf(mw, top);
-        const float corr = exp2f(mw - mn);
-        l *= corr;
-        mw = mn;
-        if (i > 0) {
-          if (QT == 1) {  // S of this tile was issued before the last P V
-            ok = __all_sync(0xffffffffu, mbar_wait(pv_done, (i - 1) & 1, p.err, (const volatile int*)s_abort));
-            if (!ok) {
-              *s_abort = 1;
-              break;
-            }
+        // ---- the maximum moves: O follows, once the products issued before are in it
+        if (__any_sync(0xffffffffu, top > mw + kLazy)) {
+          const float mn = fmaxf(mw, top);
+          const float corr = exp2f(mw - mn);
+          l *= corr;
+          mw = mn;
+          if (i > 0 || half > 0) {
+            ok = QT == 2 || i == 0 ||  // QT 2: S of this tile was issued after them
+                 paged_wait(&pv_done[j], (i - 1) & 1, p.err, (const volatile int*)s_abort);
+            if (half) ok = ok && paged_wait(&pv_half[j], i & 1, p.err, (const volatile int*)s_abort);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
             tc_fence_after();
-          }
-#pragma unroll 2
-          for (int c = 0; c < HD / 16; ++c) {
-            uint32_t x[16];
-            tmem_ld16_nowait(t_o + 16 * c, x);
-            tmem_wait_ld();
+#pragma unroll 1
+            for (int c = 0; c < HD / 16; ++c) {
+              uint32_t y[16];
+              tmem_ld16_nowait(t_o + 16 * c, y);
+              tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * corr);
-            tmem_st16(t_o + 16 * c, x);
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * corr);
+              tmem_st16(t_o + 16 * c, y);
+            }
           }
-          tmem_wait_st();
         }
-      }
-      // ---- weights, over the scores' own columns: group c's 16 scores become 8 words
-      auto weights = [&](int c, const uint32_t (&x)[16], uint32_t* w, int from, int to) {
-        const float kq = ks[c] * rowf, sh = lvs[c] - mw;
-        float2 sum = make_float2(0.f, 0.f);
+        // ---- weights, in the first columns of the tile's scores: 16 become 8 words.  The
+        // second half's words land behind the first half's, on scores that are already read
+        auto weights = [&](int c, uint32_t* w, int from, int to) {
+          const float4 f = f4[c];
+          const float kq = f.x * rowf, sh = f.y - mw;
+          float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) {
-          float2 s = make_float2(__uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-          if (!CAP) {
-            s = fma2(s, make_float2(kq, kq), make_float2(sh, sh));
+          for (int e = 0; e < 16; e += 2) {
+            float2 s = make_float2(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+            if (!CAP) {
+              s = fma2(s, make_float2(kq, kq), make_float2(sh, sh));
+            } else {
+              s = mul2(s, make_float2(kq, kq));
+              s.x = a.cap_log2 * tanh_ex2(s.x) + sh;
+              s.y = a.cap_log2 * tanh_ex2(s.y) + sh;
+            }
+            s.x = ex2_approx(s.x);
+            s.y = ex2_approx(s.y);
+            if (e < from || e >= to) s.x = 0.f;
+            if (e + 1 < from || e + 1 >= to) s.y = 0.f;
+            sum = add2(sum, s);
+            w[e >> 1] = cvt_h2(s.x, s.y);
+          }
+          l += (sum.x + sum.y) * f.z;
+        };
+        const uint32_t t_p = t_s + half * (KT / 4);
+#pragma unroll
+        for (int c = 0; c < HG; c += 2) {
+          uint32_t w[16];
+          if (!masked) {
+            weights(c, w, 0, 16);
+            weights(c + 1, w + 8, 0, 16);
           } else {
-            s = mul2(s, make_float2(kq, kq));
-            s.x = a.cap_log2 * tanh_ex2(s.x) + sh;
-            s.y = a.cap_log2 * tanh_ex2(s.y) + sh;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int k0 = kh + 16 * (c + h);
+              weights(c + h, w + 8 * h, lim.x - k0, f4[c + h].x >= 0.f ? lim.y - k0 : 0);
+            }
           }
-          s.x = ex2_approx(s.x);
-          s.y = ex2_approx(s.y);
-          if (e < from || e >= to) s.x = 0.f;
-          if (e + 1 < from || e + 1 >= to) s.y = 0.f;
-          sum = add2(sum, s);
-          w[e >> 1] = pack_h2(__float2half_rn(s.x), __float2half_rn(s.y));
+          tmem_st16_free(t_p + 8 * c, w);
         }
-        l += (sum.x + sum.y) * ivs[c];
-      };
-      if (!masked) {
-#pragma unroll 1
-        for (int c = 0; c < NG; c += 4) {
-          uint32_t x[4][16], w[2][16];
-#pragma unroll
-          for (int h = 0; h < 4; ++h) tmem_ld16_nowait(t_s + 16 * (c + h), x[h]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int h = 0; h < 4; ++h) weights(c + h, x[h], w[h >> 1] + 8 * (h & 1), 0, 16);
-          tmem_st16(t_s + 8 * c, w[0]);
-          tmem_st16(t_s + 8 * c + 16, w[1]);
-        }
-      } else {
-#pragma unroll 1
-        for (int c = 0; c < NG; c += 2) {
-          uint32_t x[2][16], w[16];
-          tmem_ld16_nowait(t_s + 16 * c, x[0]);
-          tmem_ld16_nowait(t_s + 16 * c + 16, x[1]);
-          tmem_wait_ld();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int k0 = key0 + 16 * (c + h);
-            weights(c + h, x[h], w + 8 * h, lim.x - k0, ks[c + h] >= 0.f ? lim.y - k0 : 0);
-          }
-          tmem_st16(t_s + 8 * c, w);
-        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[2 * sb + half]);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&p_full[sb]);
+      if (!ok) {
+        *s_abort = 1;
+        break;
+      }
     }
     // ---- the rows' output
     if (ok && nts > 0) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&o_full[j], 0, p.err, (const volatile int*)s_abort));
+      ok = __all_sync(0xffffffffu, paged_wait(&o_full[j], 0, p.err, (const volatile int*)s_abort));
       if (!ok) *s_abort = 1;
     }
     tc_fence_after();
@@ -500,63 +510,78 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     }
   } else if (warp < Cfg::SMW + Cfg::NCW) {
     // ================================================================== converter warps
-    const int ct = threadIdx.x - Cfg::SMW * 32;
-    const int chunk = ct % Cfg::CPR, rr = ct / Cfg::CPR;
+    const int cw = warp - Cfg::SMW;
+    const int chunk = lane % Cfg::CPR, rr = lane / Cfg::CPR;
     constexpr int PER = Cfg::PER;
-    // lane i < NG: the first row of group i of a tile in the pools, -1 when nothing of it is
-    // read (outside the visible keys), -2 for a refused page; and its scales
-    auto group_row = [&](int i) {
+    // unit x of this warp: rows RPU (cw + NCW x) ..
+    auto unit_row = [&](int x) { return (cw + Cfg::NCW * x) * Cfg::RPU + rr; };
+    // lane g < NG looks after group g of a tile: the table entry (only fetched here: a warp
+    // stalls at the first use of what it loads), then the group's first row in the pools, -1
+    // when nothing of it is read (outside the visible keys), -2 for a refused page
+    auto wanted = [&](int i) {
       const int k0 = (it.t0 + i) * KT + 16 * lane;
-      if (i >= nt || lane >= NG || k0 >= it.hi || k0 + 16 <= it.lo) return -1;
-      const int pg = __ldg(p.table + (size_t)it.b * p.max_pages + (k0 >> p.ps_log2));
+      return i < nt && lane < NG && k0 < it.hi && k0 + 16 > it.lo;
+    };
+    const int* table = p.table + (size_t)it.b * p.max_pages;
+    auto fetch_page = [&](int i) {
+      return wanted(i) ? __ldg(table + (((it.t0 + i) * KT + 16 * lane) >> p.ps_log2)) : 0;
+    };
+    auto group_row = [&](int i, int pg) {
+      if (!wanted(i)) return -1;
       if ((unsigned)pg >= (unsigned)p.num_pages) return -2;
-      return (pg * p.nkv + it.kvh) * p.ps + (k0 & (p.ps - 1));
+      return (pg * p.nkv + it.kvh) * p.ps + (((it.t0 + i) * KT + 16 * lane) & (p.ps - 1));
     };
     auto load = [&](const int8_t* codes, int grow, uint4 (&w)[PER]) {
 #pragma unroll
       for (int x = 0; x < PER; ++x) {
-        const int row = x * Cfg::RPP + rr;
+        const int row = unit_row(x);
         const int base = __shfl_sync(0xffffffffu, grow, row >> 4);
-        w[x] = base >= 0 ? __ldg(reinterpret_cast<const uint4*>(codes + ((size_t)base + (row & 15)) * HD) + chunk)
+        w[x] = base >= 0 && row < KT ? __ldg(reinterpret_cast<const uint4*>(codes + ((size_t)base + (row & 15)) * HD) + chunk)
                          : make_uint4(0u, 0u, 0u, 0u);
       }
     };
     // 16 codes -> 32 bytes of the swizzled fp16 tile: chunks 2 (chunk % 4), + 1 of box chunk / 4
     auto store = [&](uint8_t* tile, const uint4 (&w)[PER]) {
       uint8_t* box = tile + (chunk >> 2) * Cfg::KBOX;
-      const int c0 = 2 * (chunk & 3);
+      // lanes of odd boxes store their second half first: the eight lanes of a store's phase
+      // then hit eight different 16-byte columns
+      const int swap = (chunk >> 2) & 1, c0 = 2 * (chunk & 3) + swap;
 #pragma unroll
       for (int x = 0; x < PER; ++x) {
-        const int row = x * Cfg::RPP + rr;
-        const uint32_t u[4] = {w[x].x ^ 0x80808080u, w[x].y ^ 0x80808080u, w[x].z ^ 0x80808080u,
-                               w[x].w ^ 0x80808080u};
+        const int row = unit_row(x);
+        if ((x + 1) * Cfg::NCW > Cfg::NU && row >= KT) break;
+        const uint32_t u[4] = {(swap ? w[x].z : w[x].x) ^ 0x80808080u, (swap ? w[x].w : w[x].y) ^ 0x80808080u,
+                               (swap ? w[x].x : w[x].z) ^ 0x80808080u, (swap ? w[x].y : w[x].w) ^ 0x80808080u};
         *reinterpret_cast<uint4*>(box + row * 128 + ((c0 ^ (row & 7)) << 4)) =
             make_uint4(u8x2_to_h2(u[0], kSelLo), u8x2_to_h2(u[0], kSelHi), u8x2_to_h2(u[1], kSelLo),
                        u8x2_to_h2(u[1], kSelHi));
-        *reinterpret_cast<uint4*>(box + row * 128 + (((c0 + 1) ^ (row & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(box + row * 128 + ((c0 ^ 1 ^ (row & 7)) << 4)) =
             make_uint4(u8x2_to_h2(u[2], kSelLo), u8x2_to_h2(u[2], kSelHi), u8x2_to_h2(u[3], kSelLo),
                        u8x2_to_h2(u[3], kSelHi));
       }
     };
-    uint4 kw[PER], vw[PER];
-    int grow = group_row(0);
-    int grow1 = group_row(1);
-    load(p.k_codes, grow, kw);
-    load(p.v_codes, grow, vw);
-    float ks = 0.f, vs = 0.f;
-    auto scales = [&](int gr) {
-      ks = vs = 0.f;
+    auto scales = [&](int gr, float& k, float& v) {
+      k = v = 0.f;
       if (gr >= 0) {
-        ks = __ldg(p.k_scales + gr / p.ps);
-        vs = __ldg(p.v_scales + gr / p.ps);
+        k = __ldg(p.k_scales + (gr >> p.ps_log2));
+        v = __ldg(p.v_scales + (gr >> p.ps_log2));
       }
     };
-    const bool lead = warp == Cfg::SMW;
-    scales(grow);
+    // in flight: the codes and scales of tile i + 1, the table entries of tile i + 2
+    uint4 kw[PER], vw[PER];
+    float ks, vs, ks1, vs1;
+    int pg2 = fetch_page(1);
+    int grow = group_row(0, fetch_page(0)), grow1 = group_row(1, pg2);
+    load(p.k_codes, grow, kw);
+    load(p.v_codes, grow, vw);
+    scales(grow, ks, vs);
+    const bool lead = cw == 0;
     for (int i = 0; i < nt; ++i) {
       const int st = i % NST, sc = i % NSC;
       const uint32_t ph = ((i / NST) & 1) ^ 1;
-      bool ok = i < NST || mbar_wait(&k_free[st], ph, p.err, (const volatile int*)s_abort);
+      pg2 = fetch_page(i + 2);
+      scales(grow1, ks1, vs1);
+      bool ok = i < NST || paged_wait(&k_free[st], ph, p.err, (const volatile int*)s_abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
         *s_abort = 1;
@@ -566,10 +591,9 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
         const bool bad = grow == -2;
         if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, kErrBadPosition);
         if (lane < NG) {
-          s_ks[sc * NG + lane] = grow >= 0 ? ks : -1.f;
-          const float lv = vs > 0.f ? log2f(vs) : kZeroLvs;
-          s_lvs[sc * NG + lane] = lv;
-          s_ivs[sc * NG + lane] = vs > 0.f ? 1.f / vs : 1.2676506e30f;  // 2^100
+          const bool live = vs > 0.f;
+          s_sc[sc * NG + lane] = make_float4(grow >= 0 ? ks : -1.f, live ? log2f(vs) : kZeroLvs,
+                                             live ? 1.f / vs : 1.2676506e30f /* 2^100 */, 0.f);
         }
         const bool any_bad = __any_sync(0xffffffffu, bad);
         if (lane == 0) s_flag[sc] = any_bad;
@@ -581,7 +605,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&k_full[st]);
       load(p.k_codes, grow1, kw);
-      ok = i < NST || mbar_wait(&v_free[st], ph, p.err, (const volatile int*)s_abort);
+      ok = i < NST || paged_wait(&v_free[st], ph, p.err, (const volatile int*)s_abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
         *s_abort = 1;
@@ -592,7 +616,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       if (zero) {
 #pragma unroll
         for (int x = 0; x < PER; ++x)
-          if (zero >> ((x * Cfg::RPP + rr) >> 4) & 1u) vw[x] = make_uint4(0u, 0u, 0u, 0u);
+          if (zero >> (unit_row(x) >> 4) & 1u) vw[x] = make_uint4(0u, 0u, 0u, 0u);
       }
       store(v_s + st * Cfg::KTILE, vw);
       fence_proxy_async_smem();
@@ -600,11 +624,14 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       if (lane == 0) mbar_arrive(&v_full[st]);
       load(p.v_codes, grow1, vw);
       grow = grow1;
-      scales(grow);
-      grow1 = group_row(i + 2);
+      grow1 = group_row(i + 2, pg2);
+      ks = ks1;
+      vs = vs1;
     }
-  } else if (lane == 0) {
+  } else {
     // ================================================================== MMA issuer
+    if (lane == 0) {
+    const volatile int* ab = (const volatile int*)s_abort;
     constexpr uint32_t idS = idesc_f16_f32(128, KT, false);
     constexpr uint32_t idO = idesc_f16_f32(128, HD, true);
     const uint32_t qa = smem_u32(q_s), ka = smem_u32(k_s), va = smem_u32(v_s);
@@ -616,26 +643,32 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
                    smem_desc_sw128(kb + (kk >> 2) * Cfg::KBOX + (kk & 3) * 32), idS, kk != 0);
       tc_commit(&s_full[sb]);
     };
-    auto issue_pv = [&](int i, int j, int sb) {
+    // O += P V of tile i in two halves, as the softmax hands them over (phase `ph`)
+    auto issue_pv = [&](int i, int j, int sb, uint32_t ph) {
       const uint32_t vb = va + (i % NST) * Cfg::KTILE;
+      for (int half = 0; half < 2; ++half) {
+        if (!paged_wait(&p_full[2 * sb + half], ph, p.err, ab)) return false;
+        tc_fence_after();
 #pragma unroll
-      for (int kk = 0; kk < KT / 16; ++kk)
-        tc_mma_f16_ts(tmem + Cfg::O_COL + j * HD, tmem + sb * Cfg::S_COLS + kk * 8,
-                      smem_desc_sw128_mn(vb + kk * 2048, Cfg::KBOX), idO, (i | kk) != 0);
+        for (int x = 0; x < KT / 32; ++x) {
+          const int kk = half * (KT / 32) + x;
+          tc_mma_f16_ts(tmem + Cfg::O_COL + j * HD, tmem + sb * Cfg::S_COLS + kk * 8,
+                        smem_desc_sw128_mn(vb + kk * 2048, Cfg::KBOX), idO, (i | kk) != 0);
+        }
+        tc_commit(half ? &pv_done[j] : &pv_half[j]);
+      }
+      return true;
     };
-    const volatile int* ab = (const volatile int*)s_abort;
-    bool ok = mbar_wait(q_full, 0, p.err, ab);
+    bool ok = paged_wait(q_full, 0, p.err, ab);
     if (QT == 2) {
       // tile i: P V of tile i - 1, then S of tile i, for each row tile in turn
       for (int i = 0; ok && i <= nt; ++i) {
-        if (i < nt) ok = mbar_wait(&k_full[i % NST], (i / NST) & 1, p.err, ab);
-        if (ok && i > 0) ok = mbar_wait(&v_full[(i - 1) % NST], ((i - 1) / NST) & 1, p.err, ab);
+        if (i < nt) ok = paged_wait(&k_full[i % NST], (i / NST) & 1, p.err, ab);
+        if (ok && i > 0) ok = paged_wait(&v_full[(i - 1) % NST], ((i - 1) / NST) & 1, p.err, ab);
         for (int j = 0; ok && j < tiles; ++j) {
           if (i > 0) {
-            ok = mbar_wait(&p_full[j], (i - 1) & 1, p.err, ab);
+            ok = issue_pv(i - 1, j, j, (i - 1) & 1);
             if (!ok) break;
-            tc_fence_after();
-            issue_pv(i - 1, j, j);
             if (i == nt) tc_commit(&o_full[j]);
           }
           tc_fence_after();
@@ -649,19 +682,16 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       // S of tile i + 1 runs while tile i is in its softmax
       for (int i = -1; ok && i < nt; ++i) {
         if (i + 1 < nt) {
-          ok = mbar_wait(&k_full[(i + 1) % NST], ((i + 1) / NST) & 1, p.err, ab);
+          ok = paged_wait(&k_full[(i + 1) % NST], ((i + 1) / NST) & 1, p.err, ab);
           if (!ok) break;
           tc_fence_after();
           issue_s(i + 1, 0, (i + 1) & 1);
           tc_commit(&k_free[(i + 1) % NST]);
         }
         if (i >= 0) {
-          ok = mbar_wait(&v_full[i % NST], (i / NST) & 1, p.err, ab) &&
-               mbar_wait(&p_full[i & 1], (i >> 1) & 1, p.err, ab);
+          ok = paged_wait(&v_full[i % NST], (i / NST) & 1, p.err, ab) &&
+               issue_pv(i, 0, i & 1, (i >> 1) & 1);
           if (!ok) break;
-          tc_fence_after();
-          issue_pv(i, 0, i & 1);
-          tc_commit(pv_done);
           if (i == nt - 1) tc_commit(&o_full[0]);
           tc_commit(&v_free[i % NST]);
         }
@@ -671,7 +701,8 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       // what was issued finishes before the tensor memory goes
       *s_abort = 1;
       tc_commit(drain);
-      mbar_wait(drain, 0, p.err);
+      paged_wait(drain, 0, p.err);
+    }
     }
   }
   __syncwarp();

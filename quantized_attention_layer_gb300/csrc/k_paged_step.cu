@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
 
     for (; k < count && t0 + warp + (long long)k * NC < end; ++k) {
       const int st = k % ns;
-      if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bars[st], (k / ns) & 1, p.err))) dead = true;
+      if (!dead && !__all_sync(0xffffffffu, paged_wait(&bars[st], (k / ns) & 1, p.err))) dead = true;
       if (dead) continue;
       const Block blk = recs[st];
       if (blk.key0 >= 0) {
@@ -524,7 +524,7 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
   }
   // a warp that gave up: its copies still in flight land before the CTA may exit
   if (dead) {
-    for (int i = k > ns ? k - ns : 0; i < issued; ++i) mbar_wait(&bars[i % ns], (i / ns) & 1, p.err);
+    for (int i = k > ns ? k - ns : 0; i < issued; ++i) paged_wait(&bars[i % ns], (i / ns) & 1, p.err);
   }
 }
 
