@@ -73,15 +73,42 @@ constexpr float kZeroLvs = -100.f;  // log2 vs of a page whose scale is 0 (its c
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24) | (b_mn ? 1u << 16 : 0u);
 }
-// D[tmem] (+)= A[tmem] * B[smem desc]^T
-__device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                              uint32_t idesc, uint32_t accumulate) {
+// The MMAs and commits, executed by a whole warp of which one lane issues: operands that the
+// warp shares stay in uniform registers, where a single thread would move each one there.
+// D[tmem] (+)= A[smem desc] * B[smem desc]^T
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, e;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem desc]^T
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, e;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
@@ -218,7 +245,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
   BlockItem* s_item = reinterpret_cast<BlockItem*>(s_tmem + 1);
 
   const PagedView& p = a.p;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = p.nh / p.nkv;
   if (warp == 0) {
     BlockItem it;
@@ -365,10 +392,14 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
         if (!masked) {
 #pragma unroll
           for (int c = 0; c < HG; ++c) {
-            float gm = __uint_as_float(x[c][0]);
+            float gm = __uint_as_float(x[c][0]), g2 = __uint_as_float(x[c][1]);
 #pragma unroll
-            for (int e = 1; e < 16; ++e) gm = fmaxf(gm, __uint_as_float(x[c][e]));
-            raise(c, gm);
+            for (int e = 2; e < 14; e += 4) {
+              gm = max3(gm, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+              g2 = max3(g2, __uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3]));
+            }
+            gm = max3(gm, __uint_as_float(x[c][14]), __uint_as_float(x[c][15]));
+            raise(c, fmaxf(gm, g2));
           }
         } else {
 #pragma unroll
@@ -630,79 +661,81 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     }
   } else {
     // ================================================================== MMA issuer
-    if (lane == 0) {
-    const volatile int* ab = (const volatile int*)s_abort;
+    // a wait whose outcome the warp shares: the elections below need every lane
+    auto wait = [&](uint64_t* bar, uint32_t ph) {
+      return (bool)__all_sync(0xffffffffu, paged_wait(bar, ph, p.err, (const volatile int*)s_abort));
+    };
     constexpr uint32_t idS = idesc_f16_f32(128, KT, false);
     constexpr uint32_t idO = idesc_f16_f32(128, HD, true);
     const uint32_t qa = smem_u32(q_s), ka = smem_u32(k_s), va = smem_u32(v_s);
     auto issue_s = [&](int i, int j, int sb) {
-      const uint32_t kb = ka + (i % NST) * Cfg::KTILE, qb = qa + j * Cfg::QTILE;
+      // descriptors count addresses in 16 bytes: steps are added to the first one
+      const uint64_t kd = smem_desc_sw128(ka + (i % NST) * Cfg::KTILE), qd = smem_desc_sw128(qa + j * Cfg::QTILE);
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk)
-        tc_mma_f16(tmem + sb * Cfg::S_COLS, smem_desc_sw128(qb + (kk >> 2) * Cfg::QBOX + (kk & 3) * 32),
-                   smem_desc_sw128(kb + (kk >> 2) * Cfg::KBOX + (kk & 3) * 32), idS, kk != 0);
-      tc_commit(&s_full[sb]);
+        mma_ss(tmem + sb * Cfg::S_COLS, qd + (((kk >> 2) * Cfg::QBOX + (kk & 3) * 32) >> 4),
+               kd + (((kk >> 2) * Cfg::KBOX + (kk & 3) * 32) >> 4), idS, kk != 0);
+      mma_commit(&s_full[sb]);
     };
     // O += P V of tile i in two halves, as the softmax hands them over (phase `ph`)
     auto issue_pv = [&](int i, int j, int sb, uint32_t ph) {
-      const uint32_t vb = va + (i % NST) * Cfg::KTILE;
+      const uint64_t vd = smem_desc_sw128_mn(va + (i % NST) * Cfg::KTILE, Cfg::KBOX);
       for (int half = 0; half < 2; ++half) {
-        if (!paged_wait(&p_full[2 * sb + half], ph, p.err, ab)) return false;
+        if (!wait(&p_full[2 * sb + half], ph)) return false;
         tc_fence_after();
 #pragma unroll
         for (int x = 0; x < KT / 32; ++x) {
           const int kk = half * (KT / 32) + x;
-          tc_mma_f16_ts(tmem + Cfg::O_COL + j * HD, tmem + sb * Cfg::S_COLS + kk * 8,
-                        smem_desc_sw128_mn(vb + kk * 2048, Cfg::KBOX), idO, (i | kk) != 0);
+          mma_ts(tmem + Cfg::O_COL + j * HD, tmem + sb * Cfg::S_COLS + kk * 8,
+                 vd + ((kk * 2048) >> 4), idO, (i | kk) != 0);
         }
-        tc_commit(half ? &pv_done[j] : &pv_half[j]);
+        mma_commit(half ? &pv_done[j] : &pv_half[j]);
       }
       return true;
     };
-    bool ok = paged_wait(q_full, 0, p.err, ab);
+    bool ok = wait(q_full, 0);
     if (QT == 2) {
       // tile i: P V of tile i - 1, then S of tile i, for each row tile in turn
       for (int i = 0; ok && i <= nt; ++i) {
-        if (i < nt) ok = paged_wait(&k_full[i % NST], (i / NST) & 1, p.err, ab);
-        if (ok && i > 0) ok = paged_wait(&v_full[(i - 1) % NST], ((i - 1) / NST) & 1, p.err, ab);
+        if (i < nt) ok = wait(&k_full[i % NST], (i / NST) & 1);
+        if (ok && i > 0) ok = wait(&v_full[(i - 1) % NST], ((i - 1) / NST) & 1);
         for (int j = 0; ok && j < tiles; ++j) {
           if (i > 0) {
             ok = issue_pv(i - 1, j, j, (i - 1) & 1);
             if (!ok) break;
-            if (i == nt) tc_commit(&o_full[j]);
+            if (i == nt) mma_commit(&o_full[j]);
           }
           tc_fence_after();
           if (i < nt) issue_s(i, j, j);
         }
         if (!ok) break;
-        if (i > 0) tc_commit(&v_free[(i - 1) % NST]);
-        if (i < nt) tc_commit(&k_free[i % NST]);
+        if (i > 0) mma_commit(&v_free[(i - 1) % NST]);
+        if (i < nt) mma_commit(&k_free[i % NST]);
       }
     } else {
       // S of tile i + 1 runs while tile i is in its softmax
       for (int i = -1; ok && i < nt; ++i) {
         if (i + 1 < nt) {
-          ok = paged_wait(&k_full[(i + 1) % NST], ((i + 1) / NST) & 1, p.err, ab);
+          ok = wait(&k_full[(i + 1) % NST], ((i + 1) / NST) & 1);
           if (!ok) break;
           tc_fence_after();
           issue_s(i + 1, 0, (i + 1) & 1);
-          tc_commit(&k_free[(i + 1) % NST]);
+          mma_commit(&k_free[(i + 1) % NST]);
         }
         if (i >= 0) {
-          ok = paged_wait(&v_full[i % NST], (i / NST) & 1, p.err, ab) &&
+          ok = wait(&v_full[i % NST], (i / NST) & 1) &&
                issue_pv(i, 0, i & 1, (i >> 1) & 1);
           if (!ok) break;
-          if (i == nt - 1) tc_commit(&o_full[0]);
-          tc_commit(&v_free[i % NST]);
+          if (i == nt - 1) mma_commit(&o_full[0]);
+          mma_commit(&v_free[i % NST]);
         }
       }
     }
     if (!ok) {
       // what was issued finishes before the tensor memory goes
       *s_abort = 1;
-      tc_commit(drain);
+      mma_commit(drain);
       paged_wait(drain, 0, p.err);
-    }
     }
   }
   __syncwarp();
