@@ -16,9 +16,10 @@
 // 2^-25 below the row's largest); the page's K scale multiplies the f32 scores 16 keys at a
 // time, its V scale enters the weights' exponent:
 //   w = 2^(s + log2 vs - mw), mw the running maximum of s + log2 vs, l = sum w / vs,
-// so that P <= 2^8 whatever the scales: rounding P to fp16 costs 2^-11 of a weight, below the
-// bf16 rounding of the output.  mw moves lazily, when a row exceeds it by 2^8; then the
-// thread that owns the row rescales its O in TMEM.
+// so that rounding P to fp16 costs 2^-11 of a weight whatever the scales, below the bf16
+// rounding of the output.  mw moves lazily: a step forms its weights under the old mw, and only
+// when 16 of them add up to more than 2^12 does the row's thread find the maximum, rescale its
+// O in TMEM and form them again.  So most steps need no maximum at all.
 //
 // Roles: a warpgroup per S buffer does the softmax (a thread owns a row: no shuffles), the
 // converter warps turn int8 codes into the fp16 operand tiles (global to registers a tile
@@ -43,6 +44,7 @@ struct BlockCfg {
   static constexpr int ROWS = QT * 128;
   static constexpr int KT = HD == 256 ? 64 : 128; // keys of a tile
   static constexpr int NG = KT / 16;              // 16-key groups: one scale each
+  static constexpr int UK = 64, UPT = KT / UK;    // keys of a softmax step, steps of a tile
   static constexpr int SMW = QT * 4;              // softmax warps
   static constexpr int NCW = 15 - SMW;            // converter warps; warp 15 issues the MMAs
   static constexpr int THREADS = 512;
@@ -55,8 +57,7 @@ struct BlockCfg {
   static constexpr int NSC = 4;                   // scale slots (see sc_full)
   static constexpr int SMEM_OPS = QT * QTILE + 2 * NST * KTILE;
   static constexpr size_t SMEM = 1024 + SMEM_OPS + ROWS * 4 + NSC * (NG * 16 + 16) + 256;
-  static constexpr int S_COLS = KT;
-  static constexpr int O_COL = 2 * KT;            // TMEM: S buffers, then O tiles
+  static constexpr int O_COL = QT * 2 * UK;       // TMEM: two S buffers a row tile, then O
   static constexpr int CPR = HD / 16;             // 16-byte chunks of a row of codes
   static constexpr int RPU = 32 / CPR;            // rows of a converter's unit: 32 chunks
   static constexpr int NU = KT / RPU;             // units of a tile
@@ -67,7 +68,7 @@ struct BlockCfg {
 };
 
 constexpr float kNoMax = -1e30f;
-constexpr float kLazy = 8.f;
+constexpr float kMostWeight = 4096.f;  // the sum of 16 weights above which the maximum moves
 constexpr float kZeroLvs = -100.f;  // log2 vs of a page whose scale is 0 (its codes count as 0)
 
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
@@ -105,11 +106,6 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
           smem_u32(bar))
       : "memory");
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   float2 d;
   asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
@@ -138,16 +134,6 @@ __device__ __forceinline__ uint32_t cvt_h2(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
-}
-// tmem_st16 that other memory accesses may move across: its order against the reads of the
-// same columns is that of the volatile statements
-__device__ __forceinline__ void tmem_st16_free(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
-      "%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-      "r"(r[15]));
 }
 // tanh to about 1e-7 absolute from one exponential and one reciprocal
 __device__ __forceinline__ float tanh_ex2(float x) {
@@ -215,7 +201,7 @@ template <int HD, bool CAP>
 __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     paged_block_kernel(const PagedAttnArgs a, int splits) {
   using Cfg = BlockCfg<HD>;
-  constexpr int QT = Cfg::QT, KT = Cfg::KT, NG = Cfg::NG, HG = NG / 2, NST = Cfg::NST, NSC = Cfg::NSC;
+  constexpr int QT = Cfg::QT, KT = Cfg::KT, NG = Cfg::NG, UK = Cfg::UK, UPT = Cfg::UPT, HG = UK / 16, NST = Cfg::NST, NSC = Cfg::NSC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_align1024(smem_raw);
   uint8_t* q_s = smem;
@@ -234,12 +220,11 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
   uint64_t* sc_full = v_free + NST;   // [NSC] scales.  Slot i of tile t + NSC is written once
                                       // tile t + NSC - NST's S is done, hence after every
                                       // softmax of tile t
-  uint64_t* s_full = sc_full + NSC;   // [2] S ready
-  uint64_t* p_full = s_full + 2;      // [2][2] each half of P written
-  uint64_t* o_full = p_full + 4;      // [2] a row tile's last O += P V is complete
-  uint64_t* pv_half = o_full + 2;     // [2] O += P V of each tile's first half is complete,
-  uint64_t* pv_done = pv_half + 2;    // [2] of the whole tile
-  uint64_t* drain = pv_done + 2;      // after an abort: what was issued is complete
+  uint64_t* s_full = sc_full + NSC;   // [QT][2] a step's scores are in their buffer
+  uint64_t* p_full = s_full + 4;      // [QT][2] its weights are written
+  uint64_t* pv_done = p_full + 4;     // [QT] each step's O += P V is complete
+  uint64_t* o_full = pv_done + 2;     // [QT] the last one is
+  uint64_t* drain = o_full + 2;      // after an abort: what was issued is complete
   volatile int* s_abort = reinterpret_cast<volatile int*>(drain + 1);
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain + 1) + 1;
   BlockItem* s_item = reinterpret_cast<BlockItem*>(s_tmem + 1);
@@ -264,13 +249,13 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
         mbar_init(&v_free[i], 1);
       }
       for (int i = 0; i < NSC; ++i) mbar_init(&sc_full[i], 1);
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 2 * QT; ++i) {
         mbar_init(&s_full[i], 1);
-        mbar_init(&p_full[2 * i], 4);
-        mbar_init(&p_full[2 * i + 1], 4);
-        mbar_init(&o_full[i], 1);
-        mbar_init(&pv_half[i], 1);
+        mbar_init(&p_full[i], 4);
+      }
+      for (int i = 0; i < QT; ++i) {
         mbar_init(&pv_done[i], 1);
+        mbar_init(&o_full[i], 1);
       }
       mbar_init(drain, 1);
       *s_abort = 0;
@@ -352,94 +337,35 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
     float mw = kNoMax, l = 0.f;
     bool ok = true;
-    const int nts = j < tiles ? nt : 0;
-    for (int i = 0; i < nts; ++i) {
-      const int sb = QT == 2 ? j : i & 1;               // S buffer
-      const int ph = QT == 2 ? i & 1 : (i >> 1) & 1;    // its phase
-      const int sc = i % NSC;
-      const int key0 = (it.t0 + i) * KT;
-      const uint32_t t_s = t_lane + sb * Cfg::S_COLS;
-      const uint32_t t_o = t_lane + Cfg::O_COL + j * HD;
-      ok = paged_wait(&sc_full[sc], (i / NSC) & 1, p.err, (const volatile int*)s_abort) &&
-           paged_wait(&s_full[sb], ph, p.err, (const volatile int*)s_abort);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {
-        *s_abort = 1;
-        break;
-      }
-      tc_fence_after();
-      const float4* scale = s_sc + sc * NG;
-      const bool masked = key0 < wlo || key0 + KT > whi || s_flag[sc];
-      // two halves of the tile's keys, each with its own look at the maximum: half the scores
-      // in registers, and the MMA starts on the first half while the second is formed
+    const uint32_t t_o = t_lane + Cfg::O_COL + j * HD;
+    const int steps = j < tiles ? nt * UPT : 0;
 #pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        const uint32_t t_h = t_s + half * (KT / 2);
-        const float4* f4 = scale + half * HG;
-        const int kh = key0 + half * (KT / 2);
+    for (int u = 0; u < steps; ++u) {
+      const int sb = 2 * j + (u & 1);
+      const int i = u / UPT, sc = i % NSC;
+      const int kh = it.t0 * KT + u * UK;  // first key
+      const uint32_t t_h = t_lane + sb * UK;
+      ok = (u % UPT != 0 || paged_wait(&sc_full[sc], (i / NSC) & 1, p.err, (const volatile int*)s_abort)) &&
+           paged_wait(&s_full[sb], (u >> 1) & 1, p.err, (const volatile int*)s_abort);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      const float4* f4 = s_sc + sc * NG + (u % UPT) * HG;
+      const bool masked = kh < wlo || kh + UK > whi || s_flag[sc];
+      // the columns of group c that hold keys this row sees
+      auto from = [&](int c) { return lim.x - (kh + 16 * c); };
+      auto to = [&](int c) { return f4[c].x >= 0.f ? lim.y - (kh + 16 * c) : 0; };
+      uint32_t w[HG / 2][16];
+      float sums;
+      for (;;) {
+        // ---- weights under the present maximum: 16 scores become 8 words
         uint32_t x[HG][16];
 #pragma unroll
         for (int c = 0; c < HG; ++c) tmem_ld16_nowait(t_h + 16 * c, x[c]);
         tmem_wait_ld();
-        // ---- maximum of s + log2 vs
-        float top = -INFINITY;
-        auto raise = [&](int gr, float gm) {
-          const float4 f = f4[gr];
-          float s = gm * (f.x * rowf);
-          if (CAP) s = a.cap_log2 * tanh_ex2(s);
-          top = fmaxf(top, s + f.y);
-        };
-        if (!masked) {
-#pragma unroll
-          for (int c = 0; c < HG; ++c) {
-            float gm = __uint_as_float(x[c][0]), g2 = __uint_as_float(x[c][1]);
-#pragma unroll
-            for (int e = 2; e < 14; e += 4) {
-              gm = max3(gm, __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
-              g2 = max3(g2, __uint_as_float(x[c][e + 2]), __uint_as_float(x[c][e + 3]));
-            }
-            gm = max3(gm, __uint_as_float(x[c][14]), __uint_as_float(x[c][15]));
-            raise(c, fmaxf(gm, g2));
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < HG; ++c) {
-            // this row's keys of the group: columns [from, to)
-            const int from = lim.x - (kh + 16 * c), to = f4[c].x >= 0.f ? lim.y - (kh + 16 * c) : 0;
-            float gm = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-              if (e >= from && e < to) gm = fmaxf(gm, __uint_as_float(x[c][e]));
-            if (gm != -INFINITY) raise(c, gm);
-          }
-        }
-        // ---- the maximum moves: O follows, once the products issued before are in it
-        if (__any_sync(0xffffffffu, top > mw + kLazy)) {
-          const float mn = fmaxf(mw, top);
-          const float corr = exp2f(mw - mn);
-          l *= corr;
-          mw = mn;
-          if (i > 0 || half > 0) {
-            ok = QT == 2 || i == 0 ||  // QT 2: S of this tile was issued after them
-                 paged_wait(&pv_done[j], (i - 1) & 1, p.err, (const volatile int*)s_abort);
-            if (half) ok = ok && paged_wait(&pv_half[j], i & 1, p.err, (const volatile int*)s_abort);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 0; c < HD / 16; ++c) {
-              uint32_t y[16];
-              tmem_ld16_nowait(t_o + 16 * c, y);
-              tmem_wait_ld();
-#pragma unroll
-              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * corr);
-              tmem_st16(t_o + 16 * c, y);
-            }
-          }
-        }
-        // ---- weights, in the first columns of the tile's scores: 16 become 8 words.  The
-        // second half's words land behind the first half's, on scores that are already read
-        auto weights = [&](int c, uint32_t* w, int from, int to) {
+        float most = 0.f;
+        sums = 0.f;
+        auto weights = [&](int c, int from, int to) {
           const float4 f = f4[c];
           const float kq = f.x * rowf, sh = f.y - mw;
           float2 sum = make_float2(0.f, 0.f);
@@ -458,44 +384,75 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
             if (e < from || e >= to) s.x = 0.f;
             if (e + 1 < from || e + 1 >= to) s.y = 0.f;
             sum = add2(sum, s);
-            w[e >> 1] = cvt_h2(s.x, s.y);
+            w[c >> 1][8 * (c & 1) + (e >> 1)] = cvt_h2(s.x, s.y);
           }
-          l += (sum.x + sum.y) * f.z;
+          most = fmaxf(most, sum.x + sum.y);
+          sums += (sum.x + sum.y) * f.z;
         };
-        const uint32_t t_p = t_s + half * (KT / 4);
+        if (!masked) {
 #pragma unroll
-        for (int c = 0; c < HG; c += 2) {
-          uint32_t w[16];
-          if (!masked) {
-            weights(c, w, 0, 16);
-            weights(c + 1, w + 8, 0, 16);
-          } else {
+          for (int c = 0; c < HG; ++c) weights(c, 0, 16);
+        } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int k0 = kh + 16 * (c + h);
-              weights(c + h, w + 8 * h, lim.x - k0, f4[c + h].x >= 0.f ? lim.y - k0 : 0);
-            }
-          }
-          tmem_st16_free(t_p + 8 * c, w);
+          for (int c = 0; c < HG; ++c) weights(c, from(c), to(c));
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[2 * sb + half]);
+        if (!__any_sync(0xffffffffu, most > kMostWeight)) break;
+        // ---- rare: the maximum moves, O and l follow, the weights are formed again (once: they
+        // are then at most 1, so the warp cannot come here twice for one step)
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < HG; ++c) {
+          tmem_ld16_nowait(t_h + 16 * c, x[0]);
+          tmem_wait_ld();
+          float gm = -INFINITY;
+          const int e0 = masked ? from(c) : 0, e1 = masked ? to(c) : 16;
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (e >= e0 && e < e1) gm = fmaxf(gm, __uint_as_float(x[0][e]));
+          if (gm != -INFINITY) {
+            const float4 f = f4[c];
+            float s = gm * (f.x * rowf);
+            if (CAP) s = a.cap_log2 * tanh_ex2(s);
+            top = fmaxf(top, s + f.y);
+          }
+        }
+        const float mn = fmaxf(mw, top);
+        const float corr = exp2f(mw - mn);
+        l *= corr;
+        mw = mn;
+        if (u > 0) {
+          ok = __all_sync(0xffffffffu,
+                          paged_wait(&pv_done[j], (u - 1) & 1, p.err, (const volatile int*)s_abort));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < HD / 16; ++c) {
+            uint32_t y[16];
+            tmem_ld16_nowait(t_o + 16 * c, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * corr);
+            tmem_st16(t_o + 16 * c, y);
+          }
+        }
       }
-      if (!ok) {
-        *s_abort = 1;
-        break;
-      }
+      if (!ok) break;
+      l += sums;
+#pragma unroll
+      for (int c = 0; c < HG / 2; ++c) tmem_st16(t_h + 16 * c, w[c]);  // over the scores
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_full[sb]);
     }
+    if (!ok) *s_abort = 1;
     // ---- the rows' output
-    if (ok && nts > 0) {
+    if (ok && steps > 0) {
       ok = __all_sync(0xffffffffu, paged_wait(&o_full[j], 0, p.err, (const volatile int*)s_abort));
       if (!ok) *s_abort = 1;
     }
     tc_fence_after();
     if (ok) {
-      const uint32_t t_o = t_lane + Cfg::O_COL + j * HD;
       if (splits == 1) {
         const float f = l > 0.f ? 1.f / l : 0.f;
         const int R = it.r0 + j * 128 + r;
@@ -504,7 +461,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
 #pragma unroll 2
         for (int c = 0; c < HD / 16; ++c) {
           uint32_t x[16], w[8];
-          if (nts > 0) {
+          if (steps > 0) {
             tmem_ld16_nowait(t_o + 16 * c, x);
             tmem_wait_ld();
           } else {
@@ -522,7 +479,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
         }
       } else {
         float* rec = a.block_records + ((size_t)blockIdx.x * Cfg::ROWS + j * 128 + r) * kPagedRecord(HD);
-        if (nts > 0) {
+        if (steps > 0) {
 #pragma unroll 2
           for (int c = 0; c < HD / 16; ++c) {
             uint32_t x[16];
@@ -542,10 +499,20 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
   } else if (warp < Cfg::SMW + Cfg::NCW) {
     // ================================================================== converter warps
     const int cw = warp - Cfg::SMW;
-    const int chunk = lane % Cfg::CPR, rr = lane / Cfg::CPR;
-    constexpr int PER = Cfg::PER;
+    // a unit's lanes: four chunks of each row, then the next four: the eight lanes of a store's
+    // phase come from two rows and hit eight different 16-byte columns
+    constexpr int PER = Cfg::PER, RPU = Cfg::RPU;
+    const int rr = (lane >> 2) % RPU, chunk = (lane & 3) + 4 * (lane / (4 * RPU));
     // unit x of this warp: rows RPU (cw + NCW x) ..
-    auto unit_row = [&](int x) { return (cw + Cfg::NCW * x) * Cfg::RPU + rr; };
+    auto unit_row = [&](int x) { return (cw + Cfg::NCW * x) * RPU + rr; };
+    // where a unit's codes go: 32 bytes of the swizzled fp16 tile, columns 2 (chunk % 4) and
+    // + 1 of box chunk / 4 (the second is the first with bit 4 turned)
+    uint32_t place[PER];
+#pragma unroll
+    for (int x = 0; x < PER; ++x) {
+      const int row = unit_row(x);
+      place[x] = (chunk >> 2) * Cfg::KBOX + row * 128 + ((2 * (chunk & 3)) ^ (row & 7)) * 16;
+    }
     // lane g < NG looks after group g of a tile: the table entry (only fetched here: a warp
     // stalls at the first use of what it loads), then the group's first row in the pools, -1
     // when nothing of it is read (outside the visible keys), -2 for a refused page
@@ -562,31 +529,28 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       if ((unsigned)pg >= (unsigned)p.num_pages) return -2;
       return (pg * p.nkv + it.kvh) * p.ps + (((it.t0 + i) * KT + 16 * lane) & (p.ps - 1));
     };
+    // rows that nobody sees come from the pool's first row: finite codes of weight 0
     auto load = [&](const int8_t* codes, int grow, uint4 (&w)[PER]) {
+      const int8_t* at = codes + 16 * chunk;
+      const int grow0 = max(grow, 0);
 #pragma unroll
       for (int x = 0; x < PER; ++x) {
         const int row = unit_row(x);
-        const int base = __shfl_sync(0xffffffffu, grow, row >> 4);
-        w[x] = base >= 0 && row < KT ? __ldg(reinterpret_cast<const uint4*>(codes + ((size_t)base + (row & 15)) * HD) + chunk)
-                         : make_uint4(0u, 0u, 0u, 0u);
+        const int base = __shfl_sync(0xffffffffu, grow0, row >> 4);
+        if ((x + 1) * Cfg::NCW <= Cfg::NU || row < KT)
+          w[x] = __ldg(reinterpret_cast<const uint4*>(at + (size_t)(base + (row & 15)) * HD));
       }
     };
-    // 16 codes -> 32 bytes of the swizzled fp16 tile: chunks 2 (chunk % 4), + 1 of box chunk / 4
     auto store = [&](uint8_t* tile, const uint4 (&w)[PER]) {
-      uint8_t* box = tile + (chunk >> 2) * Cfg::KBOX;
-      // lanes of odd boxes store their second half first: the eight lanes of a store's phase
-      // then hit eight different 16-byte columns
-      const int swap = (chunk >> 2) & 1, c0 = 2 * (chunk & 3) + swap;
 #pragma unroll
       for (int x = 0; x < PER; ++x) {
-        const int row = unit_row(x);
-        if ((x + 1) * Cfg::NCW > Cfg::NU && row >= KT) break;
-        const uint32_t u[4] = {(swap ? w[x].z : w[x].x) ^ 0x80808080u, (swap ? w[x].w : w[x].y) ^ 0x80808080u,
-                               (swap ? w[x].x : w[x].z) ^ 0x80808080u, (swap ? w[x].y : w[x].w) ^ 0x80808080u};
-        *reinterpret_cast<uint4*>(box + row * 128 + ((c0 ^ (row & 7)) << 4)) =
+        if ((x + 1) * Cfg::NCW > Cfg::NU && unit_row(x) >= KT) break;
+        const uint32_t u[4] = {w[x].x ^ 0x80808080u, w[x].y ^ 0x80808080u, w[x].z ^ 0x80808080u,
+                               w[x].w ^ 0x80808080u};
+        *reinterpret_cast<uint4*>(tile + place[x]) =
             make_uint4(u8x2_to_h2(u[0], kSelLo), u8x2_to_h2(u[0], kSelHi), u8x2_to_h2(u[1], kSelLo),
                        u8x2_to_h2(u[1], kSelHi));
-        *reinterpret_cast<uint4*>(box + row * 128 + ((c0 ^ 1 ^ (row & 7)) << 4)) =
+        *reinterpret_cast<uint4*>(tile + (place[x] ^ 16)) =
             make_uint4(u8x2_to_h2(u[2], kSelLo), u8x2_to_h2(u[2], kSelHi), u8x2_to_h2(u[3], kSelLo),
                        u8x2_to_h2(u[3], kSelHi));
       }
@@ -665,70 +629,56 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     auto wait = [&](uint64_t* bar, uint32_t ph) {
       return (bool)__all_sync(0xffffffffu, paged_wait(bar, ph, p.err, (const volatile int*)s_abort));
     };
-    constexpr uint32_t idS = idesc_f16_f32(128, KT, false);
+    constexpr uint32_t idS = idesc_f16_f32(128, UK, false);
     constexpr uint32_t idO = idesc_f16_f32(128, HD, true);
     const uint32_t qa = smem_u32(q_s), ka = smem_u32(k_s), va = smem_u32(v_s);
-    auto issue_s = [&](int i, int j, int sb) {
+    // S of step u for row tile j, into its buffer
+    auto issue_s = [&](int u, int j) {
+      const int sb = 2 * j + (u & 1);
       // descriptors count addresses in 16 bytes: steps are added to the first one
-      const uint64_t kd = smem_desc_sw128(ka + (i % NST) * Cfg::KTILE), qd = smem_desc_sw128(qa + j * Cfg::QTILE);
+      const uint64_t qd = smem_desc_sw128(qa + j * Cfg::QTILE);
+      const uint64_t kd = smem_desc_sw128(ka + (u / UPT % NST) * Cfg::KTILE + (u % UPT) * (UK * 128));
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk)
-        mma_ss(tmem + sb * Cfg::S_COLS, qd + (((kk >> 2) * Cfg::QBOX + (kk & 3) * 32) >> 4),
+        mma_ss(tmem + sb * UK, qd + (((kk >> 2) * Cfg::QBOX + (kk & 3) * 32) >> 4),
                kd + (((kk >> 2) * Cfg::KBOX + (kk & 3) * 32) >> 4), idS, kk != 0);
       mma_commit(&s_full[sb]);
     };
-    // O += P V of tile i in two halves, as the softmax hands them over (phase `ph`)
-    auto issue_pv = [&](int i, int j, int sb, uint32_t ph) {
-      const uint64_t vd = smem_desc_sw128_mn(va + (i % NST) * Cfg::KTILE, Cfg::KBOX);
-      for (int half = 0; half < 2; ++half) {
-        if (!wait(&p_full[2 * sb + half], ph)) return false;
-        tc_fence_after();
+    // O += P V of step u
+    auto issue_pv = [&](int u, int j) {
+      const int sb = 2 * j + (u & 1);
+      const uint64_t vd = smem_desc_sw128_mn(va + (u / UPT % NST) * Cfg::KTILE + (u % UPT) * (UK * 128), Cfg::KBOX);
 #pragma unroll
-        for (int x = 0; x < KT / 32; ++x) {
-          const int kk = half * (KT / 32) + x;
-          mma_ts(tmem + Cfg::O_COL + j * HD, tmem + sb * Cfg::S_COLS + kk * 8,
-                 vd + ((kk * 2048) >> 4), idO, (i | kk) != 0);
-        }
-        mma_commit(half ? &pv_done[j] : &pv_half[j]);
-      }
-      return true;
+      for (int kk = 0; kk < UK / 16; ++kk)
+        mma_ts(tmem + Cfg::O_COL + j * HD, tmem + sb * UK + kk * 8, vd + ((kk * 2048) >> 4), idO,
+               (u | kk) != 0);
+      mma_commit(&pv_done[j]);
     };
     bool ok = wait(q_full, 0);
-    if (QT == 2) {
-      // tile i: P V of tile i - 1, then S of tile i, for each row tile in turn
-      for (int i = 0; ok && i <= nt; ++i) {
-        if (i < nt) ok = wait(&k_full[i % NST], (i / NST) & 1);
-        if (ok && i > 0) ok = wait(&v_full[(i - 1) % NST], ((i - 1) / NST) & 1);
+    const int steps = nt * UPT;
+    // S of step u + 1 is there before the softmax of step u ends: the row tiles' softmaxes run
+    // without a break, the products of one behind the other's
+    for (int u = -1; ok && u < steps; ++u) {
+      if (u + 1 < steps) {
+        const int i = (u + 1) / UPT;
+        if ((u + 1) % UPT == 0) ok = wait(&k_full[i % NST], (i / NST) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        for (int j = 0; j < tiles; ++j) issue_s(u + 1, j);
+        if ((u + 1) % UPT == UPT - 1) mma_commit(&k_free[i % NST]);
+      }
+      if (u >= 0) {
+        const int i = u / UPT;
+        if (u % UPT == 0) ok = wait(&v_full[i % NST], (i / NST) & 1);
         for (int j = 0; ok && j < tiles; ++j) {
-          if (i > 0) {
-            ok = issue_pv(i - 1, j, j, (i - 1) & 1);
-            if (!ok) break;
-            if (i == nt) mma_commit(&o_full[j]);
-          }
+          ok = wait(&p_full[2 * j + (u & 1)], (u >> 1) & 1);
+          if (!ok) break;
           tc_fence_after();
-          if (i < nt) issue_s(i, j, j);
+          issue_pv(u, j);
+          if (u == steps - 1) mma_commit(&o_full[j]);
         }
         if (!ok) break;
-        if (i > 0) mma_commit(&v_free[(i - 1) % NST]);
-        if (i < nt) mma_commit(&k_free[i % NST]);
-      }
-    } else {
-      // S of tile i + 1 runs while tile i is in its softmax
-      for (int i = -1; ok && i < nt; ++i) {
-        if (i + 1 < nt) {
-          ok = wait(&k_full[(i + 1) % NST], ((i + 1) / NST) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          issue_s(i + 1, 0, (i + 1) & 1);
-          mma_commit(&k_free[(i + 1) % NST]);
-        }
-        if (i >= 0) {
-          ok = wait(&v_full[i % NST], (i / NST) & 1) &&
-               issue_pv(i, 0, i & 1, (i >> 1) & 1);
-          if (!ok) break;
-          if (i == nt - 1) mma_commit(&o_full[0]);
-          mma_commit(&v_free[i % NST]);
-        }
+        if (u % UPT == UPT - 1) mma_commit(&v_free[i % NST]);
       }
     }
     if (!ok) {
