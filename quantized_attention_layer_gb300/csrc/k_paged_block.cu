@@ -57,7 +57,9 @@ struct BlockCfg {
   static constexpr int NSC = 4;                   // scale slots (see sc_full)
   static constexpr int SMEM_OPS = QT * QTILE + 2 * NST * KTILE;
   static constexpr size_t SMEM = 1024 + SMEM_OPS + ROWS * 4 + NSC * (NG * 16 + 16) + 256;
-  static constexpr int O_COL = QT * 2 * UK;       // TMEM: two S buffers a row tile, then O
+  // scores of one MMA: a whole tile of keys, or (hd 256) a step, in the other of two buffers
+  static constexpr int SN = QT == 2 ? KT : UK;
+  static constexpr int O_COL = QT * 2 * UK;       // TMEM: two steps' S a row tile, then O
   static constexpr int CPR = HD / 16;             // 16-byte chunks of a row of codes
   static constexpr int RPU = 32 / CPR;            // rows of a converter's unit: 32 chunks
   static constexpr int NU = KT / RPU;             // units of a tile
@@ -220,7 +222,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
   uint64_t* sc_full = v_free + NST;   // [NSC] scales.  Slot i of tile t + NSC is written once
                                       // tile t + NSC - NST's S is done, hence after every
                                       // softmax of tile t
-  uint64_t* s_full = sc_full + NSC;   // [QT][2] a step's scores are in their buffer
+  uint64_t* s_full = sc_full + NSC;   // QT 2: [QT] a tile's scores are there; QT 1: [2] a step's
   uint64_t* p_full = s_full + 4;      // [QT][2] its weights are written
   uint64_t* pv_done = p_full + 4;     // [QT] each step's O += P V is complete
   uint64_t* o_full = pv_done + 2;     // [QT] the last one is
@@ -249,10 +251,8 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
         mbar_init(&v_free[i], 1);
       }
       for (int i = 0; i < NSC; ++i) mbar_init(&sc_full[i], 1);
-      for (int i = 0; i < 2 * QT; ++i) {
-        mbar_init(&s_full[i], 1);
-        mbar_init(&p_full[i], 4);
-      }
+      for (int i = 0; i < 2; ++i) mbar_init(&s_full[i], 1);
+      for (int i = 0; i < 2 * QT; ++i) mbar_init(&p_full[i], 4);
       for (int i = 0; i < QT; ++i) {
         mbar_init(&pv_done[i], 1);
         mbar_init(&o_full[i], 1);
@@ -345,8 +345,11 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       const int i = u / UPT, sc = i % NSC;
       const int kh = it.t0 * KT + u * UK;  // first key
       const uint32_t t_h = t_lane + sb * UK;
-      ok = (u % UPT != 0 || paged_wait(&sc_full[sc], (i / NSC) & 1, p.err, (const volatile int*)s_abort)) &&
-           paged_wait(&s_full[sb], (u >> 1) & 1, p.err, (const volatile int*)s_abort);
+      if (u % UPT == 0) {
+        ok = paged_wait(&sc_full[sc], (i / NSC) & 1, p.err, (const volatile int*)s_abort) &&
+             (QT == 2 ? paged_wait(&s_full[j], i & 1, p.err, (const volatile int*)s_abort)
+                      : paged_wait(&s_full[u & 1], (u >> 1) & 1, p.err, (const volatile int*)s_abort));
+      }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -629,56 +632,71 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     auto wait = [&](uint64_t* bar, uint32_t ph) {
       return (bool)__all_sync(0xffffffffu, paged_wait(bar, ph, p.err, (const volatile int*)s_abort));
     };
-    constexpr uint32_t idS = idesc_f16_f32(128, UK, false);
+    constexpr uint32_t idS = idesc_f16_f32(128, Cfg::SN, false);
     constexpr uint32_t idO = idesc_f16_f32(128, HD, true);
     const uint32_t qa = smem_u32(q_s), ka = smem_u32(k_s), va = smem_u32(v_s);
-    // S of step u for row tile j, into its buffer
-    auto issue_s = [&](int u, int j) {
-      const int sb = 2 * j + (u & 1);
+    // S = Q K^T for row tile j: of tile x, or (QT 1) of step x, its tile
+    auto issue_s = [&](int x, int j) {
+      const uint32_t d = tmem + (QT == 2 ? 2 * j : x & 1) * UK;
       // descriptors count addresses in 16 bytes: steps are added to the first one
-      const uint64_t qd = smem_desc_sw128(qa + j * Cfg::QTILE);
-      const uint64_t kd = smem_desc_sw128(ka + (u / UPT % NST) * Cfg::KTILE + (u % UPT) * (UK * 128));
+      const uint64_t qd = smem_desc_sw128(qa + j * Cfg::QTILE), kd = smem_desc_sw128(ka + x % NST * Cfg::KTILE);
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk)
-        mma_ss(tmem + sb * UK, qd + (((kk >> 2) * Cfg::QBOX + (kk & 3) * 32) >> 4),
+        mma_ss(d, qd + (((kk >> 2) * Cfg::QBOX + (kk & 3) * 32) >> 4),
                kd + (((kk >> 2) * Cfg::KBOX + (kk & 3) * 32) >> 4), idS, kk != 0);
-      mma_commit(&s_full[sb]);
+      mma_commit(&s_full[QT == 2 ? j : x & 1]);
     };
-    // O += P V of step u
+    // O += P V of step u, once its weights are there
     auto issue_pv = [&](int u, int j) {
       const int sb = 2 * j + (u & 1);
       const uint64_t vd = smem_desc_sw128_mn(va + (u / UPT % NST) * Cfg::KTILE + (u % UPT) * (UK * 128), Cfg::KBOX);
+      if (!wait(&p_full[sb], (u >> 1) & 1)) return false;
+      tc_fence_after();
 #pragma unroll
       for (int kk = 0; kk < UK / 16; ++kk)
         mma_ts(tmem + Cfg::O_COL + j * HD, tmem + sb * UK + kk * 8, vd + ((kk * 2048) >> 4), idO,
                (u | kk) != 0);
       mma_commit(&pv_done[j]);
+      return true;
     };
     bool ok = wait(q_full, 0);
-    const int steps = nt * UPT;
-    // S of step u + 1 is there before the softmax of step u ends: the row tiles' softmaxes run
-    // without a break, the products of one behind the other's
-    for (int u = -1; ok && u < steps; ++u) {
-      if (u + 1 < steps) {
-        const int i = (u + 1) / UPT;
-        if ((u + 1) % UPT == 0) ok = wait(&k_full[i % NST], (i / NST) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        for (int j = 0; j < tiles; ++j) issue_s(u + 1, j);
-        if ((u + 1) % UPT == UPT - 1) mma_commit(&k_free[i % NST]);
-      }
-      if (u >= 0) {
-        const int i = u / UPT;
-        if (u % UPT == 0) ok = wait(&v_full[i % NST], (i / NST) & 1);
+    if (QT == 2) {
+      // tile i: P V of tile i - 1, then S of tile i over it, for one row tile while the other is
+      // in its softmax
+      for (int i = 0; ok && i <= nt; ++i) {
+        if (i > 0) ok = wait(&v_full[(i - 1) % NST], ((i - 1) / NST) & 1);
         for (int j = 0; ok && j < tiles; ++j) {
-          ok = wait(&p_full[2 * j + (u & 1)], (u >> 1) & 1);
-          if (!ok) break;
-          tc_fence_after();
-          issue_pv(u, j);
-          if (u == steps - 1) mma_commit(&o_full[j]);
+          if (i > 0) {
+            ok = issue_pv(UPT * (i - 1), j) && issue_pv(UPT * (i - 1) + 1, j);
+            if (ok && i == nt) mma_commit(&o_full[j]);
+          }
+          if (i < nt) {
+            if (ok && j == 0) ok = wait(&k_full[i % NST], (i / NST) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(i, j);
+          }
         }
         if (!ok) break;
-        if (u % UPT == UPT - 1) mma_commit(&v_free[i % NST]);
+        if (i > 0) mma_commit(&v_free[(i - 1) % NST]);
+        if (i < nt) mma_commit(&k_free[i % NST]);
+      }
+    } else {
+      // S of step i + 1 runs while step i is in its softmax
+      for (int i = -1; ok && i < nt; ++i) {
+        if (i + 1 < nt) {
+          ok = wait(&k_full[(i + 1) % NST], ((i + 1) / NST) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(i + 1, 0);
+          mma_commit(&k_free[(i + 1) % NST]);
+        }
+        if (i >= 0) {
+          ok = wait(&v_full[i % NST], (i / NST) & 1) && issue_pv(i, 0);
+          if (!ok) break;
+          if (i == nt - 1) mma_commit(&o_full[0]);
+          mma_commit(&v_free[i % NST]);
+        }
       }
     }
     if (!ok) {
