@@ -150,6 +150,12 @@ struct BlockItem {
   int lo, hi;                 // keys that some row sees
   int t0, t1;                 // key tiles of this CTA
 };
+// x / G for 0 <= x < 2^29 and G <= 8: x ceil(2^32 / G) >> 32 is exact there
+struct DivG {
+  uint32_t magic;
+  __device__ __forceinline__ explicit DivG(int G) : magic(G > 1 ? 0xffffffffu / (uint32_t)G + 1u : 0u) {}
+  __device__ __forceinline__ int operator()(int x) const { return magic ? (int)__umulhi((uint32_t)x, magic) : x; }
+};
 // lower and upper limit of the keys row r (token r / G) sees
 __device__ __forceinline__ int2 row_keys(const PagedAttnArgs& a, const BlockItem& it, int tok) {
   const int P = it.len - it.n + tok;
@@ -280,41 +286,48 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     // ================================================================== softmax warps
     const int j = warp >> 2;  // row tile
     const int quad = warp & 3;
-    // ---- queries: a warp's 32 rows, CPR2 lanes a row with 8 dims each
+    const DivG divg(G);
+    // ---- queries: a warp's 32 rows, L lanes a row with 8 dims each; every load of a round in
+    // flight at once
     {
       constexpr int L = HD / 8 < 32 ? HD / 8 : 32;  // lanes of a row
-      constexpr int RPI = 32 / L;                   // rows at once
+      constexpr int RPI = 32 / L;                   // rows of an instruction
+      constexpr int NI = 32 / RPI, NB = NI < 16 ? NI : 16;
       const int c = lane % L;
-#pragma unroll 4
-      for (int i = 0; i < 32 / RPI; ++i) {
-        const int r = quad * 32 + i * RPI + lane / L;  // row of the tile
-        const int R = it.r0 + j * 128 + r;
-        const bool on = j * 128 + r < it.rows;
-        uint4 w = make_uint4(0u, 0u, 0u, 0u);
-        if (on) {
-          const int tok = R / G, h = it.kvh * G + R - tok * G;
-          w = __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
-                                                   (size_t)(it.row0 + tok) * a.q_stride +
-                                                   (size_t)h * HD + 8 * c));
+#pragma unroll 1
+      for (int i0 = 0; i0 < NI; i0 += NB) {
+        uint4 w[NB];
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int r = quad * 32 + (i0 + i) * RPI + lane / L;  // row of the tile
+          const int R = it.r0 + j * 128 + r, tok = divg(R);
+          w[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (j * 128 + r < it.rows)
+            w[i] = __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
+                                                        (size_t)(it.row0 + tok) * a.q_stride +
+                                                        (size_t)(it.kvh * G + R - tok * G) * HD + 8 * c));
         }
-        // largest exponent of the row (bf16 exponent bits of either half)
-        uint32_t e = 0;
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int x = 0; x < 4; ++x) e = max(e, max((ww[x] >> 7) & 255u, (ww[x] >> 23) & 255u));
+        for (int i = 0; i < NB; ++i) {
+          const int r = quad * 32 + (i0 + i) * RPI + lane / L;
+          // largest exponent of the row (the bf16 exponent bits of either half)
+          uint32_t e = 0;
+          const uint32_t ww[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-        for (int o = 1; o < L; o <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
-        e = min(max(e, 1u), 252u);
-        const float down = __uint_as_float((254u - e) << 23);
-        uint32_t hw[4];
+          for (int x = 0; x < 4; ++x) e = max(e, max((ww[x] >> 7) & 255u, (ww[x] >> 23) & 255u));
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          hw[x] = pack_h2(__float2half_rn(__uint_as_float(ww[x] << 16) * down),
-                          __float2half_rn(__uint_as_float(ww[x] & 0xffff0000u) * down));
-        const int box = c >> 3, ch = c & 7;
-        *reinterpret_cast<uint4*>(q_s + j * Cfg::QTILE + box * Cfg::QBOX + r * 128 +
-                                  ((ch ^ (r & 7)) << 4)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
-        if (c == 0) s_rowf[j * 128 + r] = __uint_as_float(e << 23) * a.qscale;
+          for (int o = 1; o < L; o <<= 1) e = max(e, __shfl_xor_sync(0xffffffffu, e, o));
+          e = min(max(e, 1u), 252u);
+          const float down = __uint_as_float((254u - e) << 23);
+          uint32_t hw[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            hw[x] = cvt_h2(__uint_as_float(ww[x] << 16) * down, __uint_as_float(ww[x] & 0xffff0000u) * down);
+          const int box = c >> 3, ch = c & 7;
+          *reinterpret_cast<uint4*>(q_s + j * Cfg::QTILE + box * Cfg::QBOX + r * 128 +
+                                    ((ch ^ (r & 7)) << 4)) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+          if (c == 0) s_rowf[j * 128 + r] = __uint_as_float(e << 23) * a.qscale;
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
@@ -323,7 +336,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     // ---- this thread's row
     const int r = quad * 32 + lane;
     const bool on = j * 128 + r < it.rows;
-    const int tok = (it.r0 + j * 128 + r) / G;
+    const int tok = divg(it.r0 + j * 128 + r);
     int2 lim = on ? row_keys(a, it, tok) : make_int2(0, 0);
     if (lim.y > it.len) lim.y = it.len;
     // keys that every row of the warp sees: [wlo, whi)
@@ -360,9 +373,49 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       auto to = [&](int c) { return f4[c].x >= 0.f ? lim.y - (kh + 16 * c) : 0; };
       uint32_t w[HG / 2][16];
       float sums;
-      for (;;) {
-        // ---- weights under the present maximum: 16 scores become 8 words
+      bool raise = u == 0;  // there is no maximum yet
+      for (int round = 0; round < 2; ++round) {
         uint32_t x[HG][16];
+        if (raise) {
+          // ---- rare: the maximum moves, O and l follow
+          float top = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < HG; ++c) {
+            tmem_ld16_nowait(t_h + 16 * c, x[0]);
+            tmem_wait_ld();
+            float gm = -INFINITY;
+            const int e0 = masked ? from(c) : 0, e1 = masked ? to(c) : 16;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              if (e >= e0 && e < e1) gm = fmaxf(gm, __uint_as_float(x[0][e]));
+            if (gm != -INFINITY) {
+              const float4 f = f4[c];
+              float s = gm * (f.x * rowf);
+              if (CAP) s = a.cap_log2 * tanh_ex2(s);
+              top = fmaxf(top, s + f.y);
+            }
+          }
+          const float mn = fmaxf(mw, top);
+          const float corr = exp2f(mw - mn);
+          l *= corr;
+          mw = mn;
+          if (u > 0) {
+            ok = __all_sync(0xffffffffu,
+                            paged_wait(&pv_done[j], (u - 1) & 1, p.err, (const volatile int*)s_abort));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < HD / 16; ++c) {
+              uint32_t y[16];
+              tmem_ld16_nowait(t_o + 16 * c, y);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * corr);
+              tmem_st16(t_o + 16 * c, y);
+            }
+          }
+        }
+        // ---- weights under the present maximum: 16 scores become 8 words
 #pragma unroll
         for (int c = 0; c < HG; ++c) tmem_ld16_nowait(t_h + 16 * c, x[c]);
         tmem_wait_ld();
@@ -399,45 +452,10 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
 #pragma unroll
           for (int c = 0; c < HG; ++c) weights(c, from(c), to(c));
         }
-        if (!__any_sync(0xffffffffu, most > kMostWeight)) break;
-        // ---- rare: the maximum moves, O and l follow, the weights are formed again (once: they
-        // are then at most 1, so the warp cannot come here twice for one step)
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < HG; ++c) {
-          tmem_ld16_nowait(t_h + 16 * c, x[0]);
-          tmem_wait_ld();
-          float gm = -INFINITY;
-          const int e0 = masked ? from(c) : 0, e1 = masked ? to(c) : 16;
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (e >= e0 && e < e1) gm = fmaxf(gm, __uint_as_float(x[0][e]));
-          if (gm != -INFINITY) {
-            const float4 f = f4[c];
-            float s = gm * (f.x * rowf);
-            if (CAP) s = a.cap_log2 * tanh_ex2(s);
-            top = fmaxf(top, s + f.y);
-          }
-        }
-        const float mn = fmaxf(mw, top);
-        const float corr = exp2f(mw - mn);
-        l *= corr;
-        mw = mn;
-        if (u > 0) {
-          ok = __all_sync(0xffffffffu,
-                          paged_wait(&pv_done[j], (u - 1) & 1, p.err, (const volatile int*)s_abort));
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < HD / 16; ++c) {
-            uint32_t y[16];
-            tmem_ld16_nowait(t_o + 16 * c, y);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * corr);
-            tmem_st16(t_o + 16 * c, y);
-          }
-        }
+        // formed again when they are too large: they are then at most 1 (up to the rounding of
+        // scores past 2^24, hence the limit on the rounds)
+        raise = __any_sync(0xffffffffu, most > kMostWeight);
+        if (!raise) break;
       }
       if (!ok) break;
       l += sums;
@@ -457,33 +475,47 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     tc_fence_after();
     if (ok) {
       if (splits == 1) {
+        // rows to bf16, through the query tile's place (its MMAs are done) so that a warp stores
+        // whole rows: 16-byte chunk c of row r at (c XOR (r % 8))
         const float f = l > 0.f ? 1.f / l : 0.f;
-        const int R = it.r0 + j * 128 + r;
-        __nv_bfloat16* dst = (__nv_bfloat16*)a.o +
-                             ((size_t)(it.row0 + tok) * p.nh + it.kvh * G + (R - tok * G)) * HD;
-#pragma unroll 2
-        for (int c = 0; c < HD / 16; ++c) {
-          uint32_t x[16], w[8];
-          if (steps > 0) {
-            tmem_ld16_nowait(t_o + 16 * c, x);
-            tmem_wait_ld();
-          } else {
+        uint8_t* stage = q_s + j * Cfg::QTILE + quad * 32 * (HD * 2);
+#pragma unroll 1
+        for (int c = 0; c < HD / 16; c += 4) {
+          uint32_t x[4][16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = 0u;
-          }
+          for (int h = 0; h < 4; ++h)
+            if (steps > 0) tmem_ld16_nowait(t_o + 16 * (c + h), x[h]);
+          tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            w[e] = pack_bf2(__float2bfloat16_rn(__uint_as_float(x[2 * e]) * f),
-                            __float2bfloat16_rn(__uint_as_float(x[2 * e + 1]) * f));
-          if (on) {
-            reinterpret_cast<uint4*>(dst + 16 * c)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            reinterpret_cast<uint4*>(dst + 16 * c)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          for (int h = 0; h < 4; ++h) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              w[e] = steps > 0 ? pack_bf2(__float2bfloat16_rn(__uint_as_float(x[h][2 * e]) * f),
+                                          __float2bfloat16_rn(__uint_as_float(x[h][2 * e + 1]) * f))
+                               : 0u;
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              *reinterpret_cast<uint4*>(stage + lane * (HD * 2) + (((2 * (c + h) + y) ^ (lane & 7)) << 4)) =
+                  make_uint4(w[4 * y], w[4 * y + 1], w[4 * y + 2], w[4 * y + 3]);
           }
+        }
+        __syncwarp();
+        constexpr int L = HD / 8;  // chunks of a row
+#pragma unroll 4
+        for (int i = lane; i < 32 * L; i += 32) {
+          const int row = i / L, c = i % L;
+          const int rr = j * 128 + quad * 32 + row;
+          if (rr >= it.rows) break;
+          const int R = it.r0 + rr, tk = divg(R);
+          *reinterpret_cast<uint4*>((__nv_bfloat16*)a.o +
+                                    ((size_t)(it.row0 + tk) * p.nh + it.kvh * G + (R - tk * G)) * HD + 8 * c) =
+              *reinterpret_cast<const uint4*>(stage + row * (HD * 2) + ((c ^ (row & 7)) << 4));
         }
       } else {
         float* rec = a.block_records + ((size_t)blockIdx.x * Cfg::ROWS + j * 128 + r) * kPagedRecord(HD);
         if (steps > 0) {
-#pragma unroll 2
+#pragma unroll 4
           for (int c = 0; c < HD / 16; ++c) {
             uint32_t x[16];
             tmem_ld16_nowait(t_o + 16 * c, x);
