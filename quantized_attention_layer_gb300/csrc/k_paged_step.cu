@@ -53,13 +53,6 @@ struct StepCfg {
 constexpr float kNoMax = -1e30f;  // "no score yet"; finite, so differences are never NaN
 constexpr float kLazy = 8.f;      // how far (log2) a score may exceed the running maximum
 
-struct Block {   // what a slot's reader needs to know of its block
-  float ks;      // K scale
-  float lvs;     // log2 of the V scale, -inf for 0
-  int key0;      // position of its first key; -1: nothing visible (no copy was issued)
-  int pad;
-};
-
 // shared address of byte `byte` of row `row` of a block's tile
 template <class Cfg>
 __device__ __forceinline__ uint32_t tile_addr(uint32_t tile, int row, int byte) {
@@ -106,14 +99,12 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int G = p.nh / p.nkv;
-  // layout: rings [NC][ns], query fragments, merge area, barriers, block records, prefix
+  // layout: rings [NC][ns], query fragments, merge area, barriers, prefix
   uint8_t* ring = smem + warp * ns * Cfg::SLOT;
   uint4* qf = reinterpret_cast<uint4*>(smem + NC * ns * Cfg::SLOT);
   float* red = reinterpret_cast<float*>(qf + KS * 32);
   uint64_t* bars = reinterpret_cast<uint64_t*>(red + Cfg::red_floats(max_rows)) + warp * Cfg::MAXNS;
-  Block* recs = reinterpret_cast<Block*>(reinterpret_cast<uint64_t*>(red + Cfg::red_floats(max_rows)) +
-                                         NC * Cfg::MAXNS) + warp * Cfg::MAXNS;
-  int* s_misc = reinterpret_cast<int*>(recs - warp * Cfg::MAXNS + NC * Cfg::MAXNS);  // [8]
+  int* s_misc = reinterpret_cast<int*>(bars + (NC - warp) * Cfg::MAXNS);            // [8]
   float* s_rowf = reinterpret_cast<float*>(s_misc + 8);                              // [8]
   int* s_warp = reinterpret_cast<int*>(s_rowf + 8);                                  // [NC]
   unsigned* pre = reinterpret_cast<unsigned*>(s_warp + NC);  // [batch + 1]: blocks (times KV heads) before each sequence
@@ -166,13 +157,15 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
 
   // ------------------------------------------------------------------ this warp's blocks
   const int count = (int)(t1 - t0 > warp ? (t1 - t0 - warp + NC - 1) / NC : 0);
-  // a batch of 32 blocks, one a lane: where it is and its scales
-  int pg_next = -2, row_next = 0, key_next = -1;  // page id (-2: none, -3: refused), TMA row
-  float ks_cur = 0.f, lvs_cur = 0.f, ks_next = 0.f, vs_next = 0.f;
+  // batches of 32 blocks, one a lane: the next one (fetched half a batch ahead), the one being
+  // copied, the one being consumed (the ring is shorter than a batch, so these two at most)
+  int pg_next = 0, row_next = 0, key_next = -1, kvh_next = 0;  // page, TMA row, first key (-1: none)
+  float ks_next = 0.f, vs_next = 0.f;
   int row_cur = 0, key_cur = -1;
-  int kvh_next = 0;
+  float ks_cur = 0.f, lvs_cur = 0.f;
+  int key_use = -1;
+  float ks_use = 0.f, lvs_use = 0.f;
   auto fetch_pages = [&](int k) {  // blocks k .. k + 31: table entries
-    pg_next = -2;
     key_next = -1;
     if (k + lane < count) {
       const long long tt = t0 + warp + (long long)(k + lane) * NC;
@@ -207,16 +200,10 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
     ks_cur = ks_next;
     lvs_cur = vs_next > 0.f ? log2f(vs_next) : -INFINITY;
   };
-  auto issue = [&](int k) {  // block k into slot k % ns
-    const int src = k & 31, st = k % ns;
-    const int key0 = __shfl_sync(0xffffffffu, key_cur, src);
-    const int row = __shfl_sync(0xffffffffu, row_cur, src);
-    const float ks = __shfl_sync(0xffffffffu, ks_cur, src);
-    const float lvs = __shfl_sync(0xffffffffu, lvs_cur, src);
+  auto issue = [&](int k, int st) {  // block k into slot st
+    const int key0 = __shfl_sync(0xffffffffu, key_cur, k & 31);
+    const int row = __shfl_sync(0xffffffffu, row_cur, k & 31);
     if (lane == 0) {
-      recs[st].ks = ks;
-      recs[st].lvs = lvs;
-      recs[st].key0 = key0;
       if (key0 >= 0) {
         uint8_t* kt = ring + st * Cfg::SLOT;
         mbar_arrive_expect_tx(&bars[st], Cfg::SLOT);
@@ -232,7 +219,7 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
   };
   // the order in which slots are filled: batches turn at multiples of 32
   int issued = 0;
-  auto advance = [&]() {
+  auto advance = [&](int st) {  // the next block, if there is one, into slot st
     if (issued >= count) return;
     if ((issued & 31) == 0) {
       turn_batch();
@@ -240,17 +227,23 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
     } else if ((issued & 31) == 16) {
       fetch_scales();
     }
-    issue(issued);
+    issue(issued, st);
     ++issued;
   };
   fetch_pages(0);
   fetch_scales();
-  for (int i = 0; i < ns; ++i) advance();
+  for (int i = 0; i < ns; ++i) advance(i);
+  // shared offsets of this lane's ldmatrix rows: rows 0..15 of a tile, 16-byte chunk c + (lane / 16)
+  uint32_t off[KS / 2];
+#pragma unroll
+  for (int c = 0; c < KS; c += 2)
+    off[c / 2] = tile_addr<Cfg>(0, ((lane >> 3) & 1) * 8 + (lane & 7), 16 * (c + (lane >> 4)));
 
   // ------------------------------------------------------------------ pieces of units
   bool dead = false;  // a wait gave up: no more reads, the barriers still match
-  int k = 0;
-  long long at = t0;  // first block of the piece
+  int k = 0, slot = 0;
+  uint32_t phase = 0;  // the next block: its number, slot and the slot's phase
+  long long at = t0;   // first block of the piece
   while (at < t1) {
     const int b = seq_of(at);
     const SeqPlan sq = plan_seq(a, b, G);
@@ -306,6 +299,9 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
     const int P = sq.len - sq.n + g / G;
     const int hi = g < rows ? (a.bidir ? sq.len : P + 1) : 0;
     const int lo = a.window ? P - a.window + 1 : 0;
+    // keys that every row sees
+    const int all_hi = a.bidir ? sq.len : sq.len - sq.n + 1;
+    const int all_lo = a.window ? sq.len - a.window : 0;
     float m = kNoMax, mw = kNoMax, l = 0.f;
     float o[KS][2][4];
 #pragma unroll
@@ -313,20 +309,28 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[c][0][e] = o[c][1][e] = 0.f;
 
-    for (; k < count && t0 + warp + (long long)k * NC < end; ++k) {
-      const int st = k % ns;
-      if (!dead && !__all_sync(0xffffffffu, paged_wait(&bars[st], (k / ns) & 1, p.err))) dead = true;
+    const int mine_end = (int)(end - t0);  // this warp's blocks of the piece: warp + k NC below it
+    for (int pos = warp + k * NC; pos < mine_end; pos += NC, ++k) {
+      const int st = slot;
+      if ((k & 31) == 0) {  // turned for the copies ns blocks ago at the latest
+        key_use = key_cur;
+        ks_use = ks_cur;
+        lvs_use = lvs_cur;
+      }
+      if (!dead && !__all_sync(0xffffffffu, paged_wait(&bars[st], phase, p.err))) dead = true;
+      if (++slot == ns) slot = 0, phase ^= 1;
       if (dead) continue;
-      const Block blk = recs[st];
-      if (blk.key0 >= 0) {
+      const int key0 = __shfl_sync(0xffffffffu, key_use, k & 31);
+      if (key0 >= 0) {
+        const float ks = __shfl_sync(0xffffffffu, ks_use, k & 31);
+        const float lvs = __shfl_sync(0xffffffffu, lvs_use, k & 31);
         const uint32_t kt = smem_u32(ring + st * Cfg::SLOT), vt = kt + Cfg::TILE;
         // S = Q K^T over 16 keys: tiles of keys 0..7 and 8..15
         float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
-        const int mrow = ((lane >> 3) & 1) * 8 + (lane & 7), mch = lane >> 4;
 #pragma unroll
         for (int c = 0; c < KS; c += 2) {
           uint32_t w[4];
-          ldmatrix_x4(tile_addr<Cfg>(kt, mrow, 16 * (c + mch)), w[0], w[1], w[2], w[3]);
+          ldmatrix_x4(kt + off[c / 2], w[0], w[1], w[2], w[3]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint4 qa = qf[(c + i) * 32 + lane];
@@ -336,23 +340,25 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
             mma_f16(s1, A4, u8x2_to_h2(x1, kSelLo), u8x2_to_h2(x1, kSelHi));
           }
         }
-        const float f = rowf * blk.ks;
+        const float f = rowf * ks;
         float s[4] = {(s0[0] + s0[2]) * f, (s0[1] + s0[3]) * f, (s1[0] + s1[2]) * f,
                       (s1[1] + s1[3]) * f};
         if (a.cap_log2 != 0.f) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[e] = a.cap_log2 * tanhf(s[e]);
         }
+        if (key0 < all_lo || key0 + 16 > all_hi) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = blk.key0 + 2 * t + (e & 1) + 8 * (e >> 1);
-          if (key >= hi || key < lo) s[e] = -INFINITY;
+          for (int e = 0; e < 4; ++e) {
+            const int key = key0 + 2 * t + (e & 1) + 8 * (e >> 1);
+            if (key >= hi || key < lo) s[e] = -INFINITY;
+          }
         }
         const float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-        if (__any_sync(0xffffffffu, top > m + kLazy || top + blk.lvs > mw + kLazy)) {
+        if (__any_sync(0xffffffffu, top > m + kLazy || top + lvs > mw + kLazy)) {
           float r = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 2));
-          const float mn = fmaxf(m, r), wn = fmaxf(mw, r + blk.lvs);
+          const float mn = fmaxf(m, r), wn = fmaxf(mw, r + lvs);
           l *= exp2f(m - mn);
           const float corr = exp2f(mw - wn);
           m = mn;
@@ -367,22 +373,22 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
         }
         uint32_t PA[4];
         {
-          const float shift = blk.lvs - mw;
-          __half ph[4], pl[4];
+          const float shift = lvs - mw;
+          l += (ex2_approx(s[0] - m) + ex2_approx(s[1] - m)) + (ex2_approx(s[2] - m) + ex2_approx(s[3] - m));
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            l += ex2_approx(s[e] - m);
-            split_f16(ex2_approx(s[e] + shift), ph[e], pl[e]);
+          for (int h = 0; h < 2; ++h) {
+            const float w0 = ex2_approx(s[2 * h] + shift), w1 = ex2_approx(s[2 * h + 1] + shift);
+            const __half2 hi2 = __floats2half2_rn(w0, w1);
+            const float2 back = __half22float2(hi2);
+            const __half2 lo2 = __floats2half2_rn(w0 - back.x, w1 - back.y);
+            PA[2 * h] = *reinterpret_cast<const uint32_t*>(&hi2);
+            PA[2 * h + 1] = *reinterpret_cast<const uint32_t*>(&lo2);
           }
-          PA[0] = pack_h2(ph[0], ph[1]);
-          PA[1] = pack_h2(pl[0], pl[1]);
-          PA[2] = pack_h2(ph[2], ph[3]);
-          PA[3] = pack_h2(pl[2], pl[3]);
         }
 #pragma unroll
         for (int c = 0; c < KS; c += 2) {
           uint32_t w[4];
-          ldmatrix_x4_trans(tile_addr<Cfg>(vt, mrow, 16 * (c + mch)), w[0], w[1], w[2], w[3]);
+          ldmatrix_x4_trans(vt + off[c / 2], w[0], w[1], w[2], w[3]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t x0 = w[2 * i] ^ 0x80808080u, x1 = w[2 * i + 1] ^ 0x80808080u;
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
       }
       // every lane's reads of the slot have fed the MMAs above: the slot may be refilled
       __syncwarp();
-      advance();
+      advance(st);
     }
 
     // ---------------------------------------------------------------- the CTA's record
@@ -533,7 +539,7 @@ cudaError_t launch_step_hd(const PagedAttnArgs& a, const CUtensorMap& tk, const 
                            long long blocks, int max_rows, int sms, cudaStream_t s) {
   using Cfg = StepCfg<HD>;
   const size_t fixed = 1024 + Cfg::QF + (size_t)Cfg::red_floats(max_rows) * 4 +
-                       Cfg::NC * Cfg::MAXNS * (8 + sizeof(Block)) + (16 + Cfg::NC + a.p.batch + 1) * 4;
+                       Cfg::NC * Cfg::MAXNS * 8 + (16 + Cfg::NC + a.p.batch + 1) * 4;
   const size_t budget = (Cfg::CPS == 2 ? 113 : 226) * 1024;
   int ns = (int)((budget - fixed) / (Cfg::NC * Cfg::SLOT));
   if (ns > Cfg::MAXNS) ns = Cfg::MAXNS;
