@@ -91,21 +91,51 @@ cudaError_t launch_paged_step(const PagedAttnArgs& a, const CUtensorMap& tk, con
 
 // ------------------------------------------------------------------ device helpers
 #ifdef __CUDACC__
+// The same by shared-window address (no generic pointer to convert in a loop).
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // mbar_wait with its limit in SM cycles (about 2 s): between two tries it reads the cycle
 // counter, a few cycles, where the nanosecond timer takes long enough to delay every hand-over
 // of a pipeline that waits on each tile
 constexpr long long kPagedWaitCycles = 4000000000ll;
-__device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, unsigned* err,
-                                           const volatile int* abort = nullptr) {
-  if (mbar_try_wait(bar, parity)) return true;
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, unsigned* err,
+                                         const volatile int* abort = nullptr) {
+  if (bar_try(bar, parity)) return true;
   const long long t0 = clock64();
   for (;;) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (bar_try(bar, parity)) return true;
     if (abort && *abort) return false;
     if (clock64() - t0 > kPagedWaitCycles) break;
   }
   atomicOr(err, kErrWaitTimeout);
   return false;
+}
+__device__ __forceinline__ bool paged_wait(uint64_t* bar, uint32_t parity, unsigned* err,
+                                           const volatile int* abort = nullptr) {
+  return bar_wait(smem_u32(bar), parity, err, abort);
+}
+// a 2-D TMA box by shared-window addresses
+__device__ __forceinline__ void box_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // four adjacent dims of an output row
 __device__ __forceinline__ void paged_store_o4(const PagedAttnArgs& a, int row, int h, int d, float4 v) {

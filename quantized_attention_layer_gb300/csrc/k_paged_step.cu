@@ -158,13 +158,12 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
   // ------------------------------------------------------------------ this warp's blocks
   const int count = (int)(t1 - t0 > warp ? (t1 - t0 - warp + NC - 1) / NC : 0);
   // batches of 32 blocks, one a lane: the next one (fetched half a batch ahead), the one being
-  // copied, the one being consumed (the ring is shorter than a batch, so these two at most)
-  int pg_next = 0, row_next = 0, key_next = -1, kvh_next = 0;  // page, TMA row, first key (-1: none)
-  float ks_next = 0.f, vs_next = 0.f;
-  int row_cur = 0, key_cur = -1;
-  float ks_cur = 0.f, lvs_cur = 0.f;
-  int key_use = -1;
-  float ks_use = 0.f, lvs_use = 0.f;
+  // copied, the one being consumed (the ring is shorter than a batch, so these two at most).
+  // TMA row and K scale are -1 for a block without a visible key or on a refused page.
+  int pg_next = 0, row_next = -1, key_next = -1, kvh_next = 0;
+  float ks_next = -1.f, vs_next = 0.f;
+  int row_cur = -1;
+  float ks_cur = -1.f, lvs_cur = 0.f, ks_use = -1.f, lvs_use = 0.f;
   auto fetch_pages = [&](int k) {  // blocks k .. k + 31: table entries
     key_next = -1;
     if (k + lane < count) {
@@ -181,7 +180,9 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
     }
   };
   auto fetch_scales = [&]() {
-    ks_next = vs_next = 0.f;
+    ks_next = -1.f;
+    vs_next = 0.f;
+    row_next = -1;
     if (key_next >= 0) {
       if ((unsigned)pg_next < (unsigned)p.num_pages) {
         const size_t u = (size_t)pg_next * p.nkv + kvh_next;
@@ -190,49 +191,41 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
         row_next = (int)u * p.ps + (key_next & (p.ps - 1));
       } else {
         atomicOr(p.err, kErrBadPosition);
-        key_next = -1;
       }
     }
   };
-  auto turn_batch = [&]() {
-    row_cur = row_next;
-    key_cur = key_next;
-    ks_cur = ks_next;
-    lvs_cur = vs_next > 0.f ? log2f(vs_next) : -INFINITY;
-  };
-  auto issue = [&](int k, int st) {  // block k into slot st
-    const int key0 = __shfl_sync(0xffffffffu, key_cur, k & 31);
-    const int row = __shfl_sync(0xffffffffu, row_cur, k & 31);
-    if (lane == 0) {
-      if (key0 >= 0) {
-        uint8_t* kt = ring + st * Cfg::SLOT;
-        mbar_arrive_expect_tx(&bars[st], Cfg::SLOT);
-#pragma unroll
-        for (int j = 0; j < Cfg::NBOX; ++j) {
-          tma_load_2d(kt + j * 16 * Cfg::BOXW, &tmk, &bars[st], j * Cfg::BOXW, row);
-          tma_load_2d(kt + Cfg::TILE + j * 16 * Cfg::BOXW, &tmv, &bars[st], j * Cfg::BOXW, row);
-        }
-      } else {
-        mbar_arrive(&bars[st]);
-      }
-    }
-  };
-  // the order in which slots are filled: batches turn at multiples of 32
+  const uint32_t ring0 = smem_u32(ring), bar0 = smem_u32(bars);
+  // the next block into the slot at `dst`, `bar`
   int issued = 0;
-  auto advance = [&](int st) {  // the next block, if there is one, into slot st
+  auto advance = [&](uint32_t dst, uint32_t bar) {
     if (issued >= count) return;
-    if ((issued & 31) == 0) {
-      turn_batch();
+    const int x = issued & 31;
+    if (x == 0) {
+      row_cur = row_next;
+      ks_cur = ks_next;
+      lvs_cur = vs_next > 0.f ? log2f(vs_next) : -INFINITY;
       fetch_pages(issued + 32);
-    } else if ((issued & 31) == 16) {
+    } else if (x == 16) {
       fetch_scales();
     }
-    issue(issued, st);
+    const int row = __shfl_sync(0xffffffffu, row_cur, x);
+    if (lane == 0) {
+      if (row >= 0) {
+        bar_expect(bar, Cfg::SLOT);
+#pragma unroll
+        for (int j = 0; j < Cfg::NBOX; ++j) {
+          box_load(dst + j * 16 * Cfg::BOXW, &tmk, bar, j * Cfg::BOXW, row);
+          box_load(dst + Cfg::TILE + j * 16 * Cfg::BOXW, &tmv, bar, j * Cfg::BOXW, row);
+        }
+      } else {
+        bar_arrive(bar);
+      }
+    }
     ++issued;
   };
   fetch_pages(0);
   fetch_scales();
-  for (int i = 0; i < ns; ++i) advance(i);
+  for (int i = 0; i < ns; ++i) advance(ring0 + i * Cfg::SLOT, bar0 + 8 * i);
   // shared offsets of this lane's ldmatrix rows: rows 0..15 of a tile, 16-byte chunk c + (lane / 16)
   uint32_t off[KS / 2];
 #pragma unroll
@@ -241,8 +234,9 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
 
   // ------------------------------------------------------------------ pieces of units
   bool dead = false;  // a wait gave up: no more reads, the barriers still match
-  int k = 0, slot = 0;
-  uint32_t phase = 0;  // the next block: its number, slot and the slot's phase
+  int pos = warp, use = 0;  // the next block: its place in the CTA's range, its lane in the batch
+  uint32_t slot = ring0, bar = bar0, phase = 0;
+  const uint32_t ring_end = ring0 + ns * Cfg::SLOT;
   long long at = t0;   // first block of the piece
   while (at < t1) {
     const int b = seq_of(at);
@@ -309,22 +303,20 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[c][0][e] = o[c][1][e] = 0.f;
 
-    const int mine_end = (int)(end - t0);  // this warp's blocks of the piece: warp + k NC below it
-    for (int pos = warp + k * NC; pos < mine_end; pos += NC, ++k) {
-      const int st = slot;
-      if ((k & 31) == 0) {  // turned for the copies ns blocks ago at the latest
-        key_use = key_cur;
+    const int mine_end = (int)(end - t0);
+    // the block at place x starts at key key_base + 16 x
+    const int key_base = (sq.lo + (int)(t0 - u0)) * 16;
+    for (; pos < mine_end; pos += NC) {
+      if (use == 0) {  // turned for the copies ns blocks ago at the latest
         ks_use = ks_cur;
         lvs_use = lvs_cur;
       }
-      if (!dead && !__all_sync(0xffffffffu, paged_wait(&bars[st], phase, p.err))) dead = true;
-      if (++slot == ns) slot = 0, phase ^= 1;
-      if (dead) continue;
-      const int key0 = __shfl_sync(0xffffffffu, key_use, k & 31);
-      if (key0 >= 0) {
-        const float ks = __shfl_sync(0xffffffffu, ks_use, k & 31);
-        const float lvs = __shfl_sync(0xffffffffu, lvs_use, k & 31);
-        const uint32_t kt = smem_u32(ring + st * Cfg::SLOT), vt = kt + Cfg::TILE;
+      if (!dead && !__all_sync(0xffffffffu, bar_wait(bar, phase, p.err))) dead = true;
+      const float ks = __shfl_sync(0xffffffffu, ks_use, use);
+      const float lvs = __shfl_sync(0xffffffffu, lvs_use, use);
+      if (!dead && ks >= 0.f) {
+        const int key0 = key_base + 16 * pos;
+        const uint32_t kt = slot, vt = slot + Cfg::TILE;
         // S = Q K^T over 16 keys: tiles of keys 0..7 and 8..15
         float s0[4] = {0.f, 0.f, 0.f, 0.f}, s1[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -355,7 +347,7 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
           }
         }
         const float top = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
-        if (__any_sync(0xffffffffu, top > m + kLazy || top + lvs > mw + kLazy)) {
+        if (__any_sync(0xffffffffu, top > fminf(m, mw - lvs) + kLazy)) {
           float r = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 2));
           const float mn = fmaxf(m, r), wn = fmaxf(mw, r + lvs);
@@ -399,7 +391,11 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
       }
       // every lane's reads of the slot have fed the MMAs above: the slot may be refilled
       __syncwarp();
-      advance(st);
+      if (!dead) advance(slot, bar);
+      use = (use + 1) & 31;
+      slot += Cfg::SLOT;
+      bar += 8;
+      if (slot == ring_end) slot = ring0, bar = bar0, phase ^= 1;
     }
 
     // ---------------------------------------------------------------- the CTA's record
@@ -530,7 +526,7 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
   }
   // a warp that gave up: its copies still in flight land before the CTA may exit
   if (dead) {
-    for (int i = k > ns ? k - ns : 0; i < issued; ++i) paged_wait(&bars[i % ns], (i / ns) & 1, p.err);
+    for (int i = issued > ns ? issued - ns : 0; i < issued; ++i) paged_wait(&bars[i % ns], (i / ns) & 1, p.err);
   }
 }
 
