@@ -51,6 +51,10 @@ struct StepCfg {
 };
 
 constexpr float kNoMax = -1e30f;  // "no score yet"; finite, so differences are never NaN
+// What a unit costs beside its blocks (queries, barriers, merge), in blocks: the ranges are
+// dealt out over blocks + this when there are about as many units as CTAs or more.  Fitted to
+// the cycles of CTAs with 3 and with 9 pieces of 64 ragged sequences: 11200 a piece, 303 a block.
+constexpr int kUnitCost = 36;
 constexpr float kLazy = 8.f;      // how far (log2) a score may exceed the running maximum
 
 // shared address of byte `byte` of row `row` of a block's tile
@@ -68,9 +72,9 @@ struct SeqPlan {
 };
 __device__ __forceinline__ SeqPlan plan_seq(const PagedAttnArgs& a, int b, int G) {
   SeqPlan s;
-  s.row0 = a.cu[b];
-  s.n = a.cu[b + 1] - s.row0;
-  s.len = a.len[b];
+  s.row0 = __ldg(a.cu + b);
+  s.n = __ldg(a.cu + b + 1) - s.row0;
+  s.len = __ldg(a.len + b);
   s.lo = 0;
   s.blocks = 0;
   if (s.n <= 0 || s.n * G > kPagedStepRows || s.row0 < 0 || s.row0 > a.total - s.n) return s;
@@ -117,9 +121,9 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
   {
     const int per = (p.batch + NC * 32 - 1) / (NC * 32);
     const int b0 = threadIdx.x * per;
-    unsigned sum = 0;
+    unsigned sum = 0, one = 0;
     for (int i = 0; i < per; ++i)
-      if (b0 + i < p.batch) sum += plan_seq(a, b0 + i, G).blocks;
+      if (b0 + i < p.batch) sum += one = plan_seq(a, b0 + i, G).blocks;
     unsigned inc = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -133,7 +137,7 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
     for (int i = 0; i < per; ++i)
       if (b0 + i < p.batch) {
         pre[b0 + i] = before;
-        before += plan_seq(a, b0 + i, G).blocks;
+        before += per == 1 ? one : (unsigned)plan_seq(a, b0 + i, G).blocks;
       }
     if (threadIdx.x == NC * 32 - 1) pre[p.batch] = before;
     __syncthreads();
@@ -143,17 +147,29 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
   long long A = (W + NC - 1) / NC;
   if (A > gridDim.x) A = gridDim.x;
   if (blockIdx.x >= A) return;
-  const long long t0 = W * blockIdx.x / A, t1 = W * (blockIdx.x + 1) / A;
-
-  // the sequence that owns block index x = t / nkv-scaled prefix: largest b, pre[b] nkv <= t
-  auto seq_of = [&](long long tt) {
+  const int cost = 2 * p.batch * p.nkv >= A ? kUnitCost : 0;
+  const long long V = W + (long long)cost * p.batch * p.nkv;  // blocks and the units' costs
+  // the last sequence b with (pre[b] + cost b) nkv <= x
+  auto seq_of = [&](long long x, int cost) {
     int lo = 0, hi = p.batch;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if ((long long)pre[mid] * p.nkv <= tt) lo = mid; else hi = mid;
+      if (((long long)pre[mid] + (long long)cost * mid) * p.nkv <= x) lo = mid; else hi = mid;
     }
     return lo;
   };
+  // blocks before place v of the costed list (a unit: its cost, then its blocks)
+  auto blocks_before = [&](long long v) {
+    const int b = seq_of(v, cost);
+    const int nb = (int)(pre[b + 1] - pre[b]);
+    if (v >= V) return W;
+    if (nb == 0) return (long long)pre[b] * p.nkv;
+    const uint32_t rem = (uint32_t)(v - ((long long)pre[b] + (long long)cost * b) * p.nkv);
+    const uint32_t kv = rem / (uint32_t)(nb + cost);
+    const int off = (int)(rem - kv * (uint32_t)(nb + cost)) - cost;
+    return (long long)pre[b] * p.nkv + (long long)kv * nb + (off > 0 ? off : 0);
+  };
+  const long long t0 = blocks_before(V * blockIdx.x / A), t1 = blocks_before(V * (blockIdx.x + 1) / A);
 
   // ------------------------------------------------------------------ this warp's blocks
   const int count = (int)(t1 - t0 > warp ? (t1 - t0 - warp + NC - 1) / NC : 0);
@@ -168,11 +184,11 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
     key_next = -1;
     if (k + lane < count) {
       const long long tt = t0 + warp + (long long)(k + lane) * NC;
-      const int b = seq_of(tt);
+      const int b = seq_of(tt, 0);
       const SeqPlan s = plan_seq(a, b, G);
-      const long long u = tt - (long long)pre[b] * p.nkv;
-      kvh_next = (int)(u / s.blocks);
-      const int key0 = (s.lo + (int)(u - (long long)kvh_next * s.blocks)) << 4;
+      const uint32_t u = (uint32_t)(tt - (long long)pre[b] * p.nkv);
+      kvh_next = (int)(u / (uint32_t)s.blocks);
+      const int key0 = (s.lo + (int)(u - (uint32_t)kvh_next * (uint32_t)s.blocks)) << 4;
       if (key0 < s.len) {
         key_next = key0;
         pg_next = __ldg(p.table + (size_t)b * p.max_pages + (key0 >> p.ps_log2));
@@ -238,41 +254,60 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
   uint32_t slot = ring0, bar = bar0, phase = 0;
   const uint32_t ring_end = ring0 + ns * Cfg::SLOT;
   long long at = t0;   // first block of the piece
+  // one row of a unit's queries (row = token * G + head) is one warp's to fetch, a piece ahead,
+  // and to turn into fragments; a lane holds quads lane, lane + 32, ... of it, zeros past its end
+  static_assert(NC == kPagedStepRows, "a warp per row");
+  constexpr int Q = (HD + 127) / 128;
+  uint2 raw[Q][2];  // four bf16 (the first two words) or f32 values each
+  auto fetch_row = [&](long long x) {
+    const int b = seq_of(x, 0);
+    const SeqPlan s = plan_seq(a, b, G);
+    const int kvh = (int)((uint32_t)(x - (long long)pre[b] * p.nkv) / (uint32_t)s.blocks);
+    const int tok = warp / G;
+    const size_t qo = (size_t)(s.row0 + tok) * a.q_stride + (size_t)(kvh * G + warp - tok * G) * HD;
+#pragma unroll
+    for (int j = 0; j < Q; ++j) {
+      const int d = 4 * (lane + 32 * j);
+      raw[j][0] = raw[j][1] = make_uint2(0u, 0u);
+      if (warp < s.n * G && d < HD) {
+        if (a.f32) {
+          const uint4 v = __ldg(reinterpret_cast<const uint4*>((const float*)a.q + qo + d));
+          raw[j][0] = make_uint2(v.x, v.y);
+          raw[j][1] = make_uint2(v.z, v.w);
+        } else {
+          raw[j][0] = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)a.q + qo + d));
+        }
+      }
+    }
+  };
+  if (t0 < t1) fetch_row(t0);
   while (at < t1) {
-    const int b = seq_of(at);
+    const int b = seq_of(at, 0);
     const SeqPlan sq = plan_seq(a, b, G);
     const long long ub = (long long)pre[b] * p.nkv;
-    const int kvh = (int)((at - ub) / sq.blocks);
+    const int kvh = (int)((uint32_t)(at - ub) / (uint32_t)sq.blocks);
     const long long u0 = ub + (long long)kvh * sq.blocks, u1 = u0 + sq.blocks;
     const long long end = u1 < t1 ? u1 : t1;
     const int rows = sq.n * G;
-    // query fragments: row r = token * G + head; warp r builds row r
-    for (int r = warp; r < kPagedStepRows; r += NC) {
-      // a lane holds quads lane, lane + 32, ... of the row; lanes past the row hold zeros
-      constexpr int Q = (HD + 127) / 128;
-      const int tok = r / G, h = kvh * G + r - tok * G;
-      const size_t qo = (size_t)(sq.row0 + tok) * a.q_stride + (size_t)h * HD;
+    {
+      const int r = warp;
       float x[Q][4];
       float top = 0.f;
 #pragma unroll
       for (int j = 0; j < Q; ++j) {
-        const int d = 4 * (lane + 32 * j);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < rows && d < HD) {
-          if (a.f32) {
-            v = __ldg(reinterpret_cast<const float4*>((const float*)a.q + qo + d));
-          } else {
-            const uint2 w = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)a.q + qo + d));
-            v = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u),
-                            __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xffff0000u));
-          }
+        if (a.f32) {
+          x[j][0] = __uint_as_float(raw[j][0].x), x[j][1] = __uint_as_float(raw[j][0].y);
+          x[j][2] = __uint_as_float(raw[j][1].x), x[j][3] = __uint_as_float(raw[j][1].y);
+        } else {
+          x[j][0] = __uint_as_float(raw[j][0].x << 16), x[j][1] = __uint_as_float(raw[j][0].x & 0xffff0000u);
+          x[j][2] = __uint_as_float(raw[j][0].y << 16), x[j][3] = __uint_as_float(raw[j][0].y & 0xffff0000u);
         }
-        x[j][0] = v.x, x[j][1] = v.y, x[j][2] = v.z, x[j][3] = v.w;
-        top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(x[j][i]));
       }
 #pragma unroll
       for (int of = 16; of > 0; of >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, of));
-      // 2^-e by its exponent bits: the row's largest component lands in [1, 8)
+    // 2^-e by its exponent bits: the row's largest component lands in [1, 8)
       const uint32_t E = min(max((__float_as_uint(top) >> 23) & 255u, 1u), 252u);
       const float down = __uint_as_float((254u - E) << 23);
 #pragma unroll
@@ -287,6 +322,7 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
       }
       if (lane == 0) s_rowf[r] = __uint_as_float(E << 23) * a.qscale;
     }
+    if (end < t1) fetch_row(end);
     __syncthreads();
     // row g: its keys [lo, hi)
     const float rowf = s_rowf[g];
@@ -466,7 +502,8 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
     }
     if (!whole) {
       // CTAs first .. last hold parts of this unit; the last to finish combines them
-      const int first = (int)(((u0 + 1) * A - 1) / W), last = (int)((u1 * A - 1) / W);
+      const long long v0 = u0 + (long long)cost * ((long long)b * p.nkv + kvh + 1);  // first block's place
+      const int first = (int)(((v0 + 1) * A - 1) / V), last = (int)(((v0 + sq.blocks) * A - 1) / V);
       const int parts = last - first + 1;
       const int unit = b * p.nkv + kvh;
       __threadfence();
@@ -482,6 +519,43 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
         auto rec = [&](int i, int r) {
           return a.records + (((size_t)(first + i) * 2 + (i == 0)) * kPagedStepRows + r) * RS;
         };
+        if (parts <= 16) {
+          // few parts: four at a time, every load of four in one round, under a running maximum
+          for (int i = threadIdx.x; i < rows * Q4; i += NC * 32) {
+            const int r = i / Q4, d4 = i - r * Q4;
+            float wx = kNoMax, mm = kNoMax, ll = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j0 = 0; j0 < parts; j0 += 4) {
+              float4 y[4], v[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float* p4 = rec(j0 + j < parts ? j0 + j : 0, r);
+                y[j] = __ldcg(reinterpret_cast<const float4*>(p4 + HD));
+                v[j] = __ldcg(reinterpret_cast<const float4*>(p4) + d4);
+                if (j0 + j >= parts) y[j] = make_float4(kNoMax, kNoMax, 0.f, 0.f);
+              }
+              const float wn = fmaxf(fmaxf(fmaxf(y[0].x, y[1].x), fmaxf(y[2].x, y[3].x)), wx);
+              const float mn = fmaxf(fmaxf(fmaxf(y[0].y, y[1].y), fmaxf(y[2].y, y[3].y)), mm);
+              const float f0 = exp2f(wx - wn);
+              ll *= exp2f(mm - mn);
+              acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+              wx = wn;
+              mm = mn;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                if (j0 + j >= parts) break;
+                ll += y[j].z * exp2f(y[j].y - mm);
+                const float f = exp2f(y[j].x - wx);
+                acc.x += f * v[j].x, acc.y += f * v[j].y, acc.z += f * v[j].z, acc.w += f * v[j].w;
+              }
+            }
+            const float f = ll > 0.f ? exp2f(wx - mm) / ll : 0.f;
+            paged_store_o4(a, sq.row0 + r / G, kvh * G + r % G, 4 * d4,
+                           make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+          }
+          at = end;
+          continue;
+        }
         float* wsm = red;  // [rows][parts]
         for (int r = warp; r < rows; r += NC) {
           float wx = kNoMax, mm = kNoMax;
