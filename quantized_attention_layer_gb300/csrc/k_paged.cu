@@ -21,15 +21,6 @@ namespace {
 
 constexpr int kAppendThreads = 512;  // most threads of an append CTA
 
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 r = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p));
   const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
@@ -46,6 +37,39 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// A row unit as it lies in memory (8 values of each half), and as values.
+template <class T>
+struct RawUnit {
+  static constexpr int W = sizeof(T) * 8 / 16;  // 16-byte words of 8 values
+  uint4 lo[W], hi[W];
+};
+template <class T>
+__device__ __forceinline__ void load_raw(const T* p, int half, bool on, RawUnit<T>& u) {
+#pragma unroll
+  for (int i = 0; i < RawUnit<T>::W; ++i) {
+    u.lo[i] = u.hi[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (on) {
+      // plain loads: the queries may be overwritten in place
+      u.lo[i] = reinterpret_cast<const uint4*>(p)[i];
+      u.hi[i] = reinterpret_cast<const uint4*>(p + half)[i];
+    }
+  }
+}
+__device__ __forceinline__ void values8(const uint4 (&r)[1], float (&v)[8]) {
+  const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void values8(const uint4 (&r)[2], float (&v)[8]) {
+  v[0] = __uint_as_float(r[0].x), v[1] = __uint_as_float(r[0].y);
+  v[2] = __uint_as_float(r[0].z), v[3] = __uint_as_float(r[0].w);
+  v[4] = __uint_as_float(r[1].x), v[5] = __uint_as_float(r[1].y);
+  v[6] = __uint_as_float(r[1].z), v[7] = __uint_as_float(r[1].w);
 }
 
 // |x| for finite x, 0 for NaN and infinities
@@ -155,11 +179,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
   const int j = (start >> p.ps_log2) + (a.single ? 0 : item - ((row0 >> p.ps_log2) + 2 * b));
   const int page0 = j << p.ps_log2;  // position of the page's slot 0
   if (page0 >= start + n) return;
-  const int page = p.table[(size_t)b * p.max_pages + j];
-  if ((unsigned)page >= (unsigned)p.num_pages) {
-    if (threadIdx.x == 0) atomicOr(p.err, kErrBadPosition);
-    return;
-  }
+  const int page = __ldg(p.table + (size_t)b * p.max_pages + j);  // checked below: the rows load meanwhile
   const int first = max(start - page0, 0), last = min(start + n - page0, ps);
   const int c = threadIdx.x % U, slot0 = threadIdx.x / U;
   const int rstep = blockDim.x / U;
@@ -168,10 +188,27 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
   const int kv1 = min(kv0 + a.kv_per_cta, p.nkv);
   const long long tok0 = (long long)row0 + page0 - start;  // row of slot 0
   const int warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+  auto written = [&](int slot) { return slot >= first && slot < last; };
+  auto load_kv = [&](int kv, int slot, RawUnit<T>& k, RawUnit<T>& v) {
+    const bool on = written(slot) && kv < kv1;
+    load_raw((const T*)a.k + (tok0 + slot) * a.k_stride + kv * HD + 8 * c, HD / 2, on, k);
+    load_raw((const T*)a.v + (tok0 + slot) * a.v_stride + kv * HD + 8 * c, HD / 2, on, v);
+  };
+  // QC query heads at a time: their loads are in flight together
+  constexpr int QC = sizeof(T) == 2 ? 4 : 2;
+  const int q0 = kv0 * G, q1 = kv1 * G;
+  auto load_q = [&](int h, int slot, RawUnit<T> (&q)[QC]) {
+#pragma unroll
+    for (int i = 0; i < QC; ++i)
+      load_raw((const T*)a.q + (tok0 + slot) * a.q_stride + (h + i) * HD + 8 * c, HD / 2,
+               a.q && written(slot) && h + i < q1, q[i]);
+  };
+  RawUnit<T> rk, rv;
+  if (!BIG) load_kv(kv0, slot0, rk, rv);
 
   float cs[8], sn[8];
   for (int slot = slot0; slot < ps; slot += rstep) {
-    if (slot < first || slot >= last) continue;
+    if (!written(slot)) continue;
 #pragma unroll
     for (int i = 0; i < 8; ++i) rope_cs(page0 + slot, a.rope_g[8 * c + i], cs[i], sn[i]);
     if (BIG) {
@@ -180,25 +217,22 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
         s_turn[(4 * slot + i) * U + c] = make_float4(cs[2 * i], sn[2 * i], cs[2 * i + 1], sn[2 * i + 1]);
     }
   }  // a thread reads back only what it wrote itself: no barrier
+  if ((unsigned)page >= (unsigned)p.num_pages) {
+    if (threadIdx.x == 0) atomicOr(p.err, kErrBadPosition);
+    return;
+  }
 
-  // rows of head kv at `slot`, normed and rotated; zeros outside the written range.  Every
-  // lane of a warp calls it together (the norm's sum goes over the lanes of a row).
-  auto kv_rows = [&](int kv, int slot, float (&kl)[8], float (&kh)[8], float (&vl)[8],
-                     float (&vh)[8]) {
-    const bool on = slot >= first && slot < last;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) kl[i] = kh[i] = vl[i] = vh[i] = 0.f;
-    if (on) {
-      const T* kp = (const T*)a.k + (tok0 + slot) * a.k_stride + kv * HD + 8 * c;
-      const T* vp = (const T*)a.v + (tok0 + slot) * a.v_stride + kv * HD + 8 * c;
-      load8(kp, kl);
-      load8(kp + HD / 2, kh);
-      load8(vp, vl);
-      load8(vp + HD / 2, vh);
-    }
+  // the K and V values of a unit, normed and rotated.  Every lane of a warp calls it together
+  // (the norm's sum goes over the lanes of a row).
+  auto kv_values = [&](int slot, const RawUnit<T>& k, const RawUnit<T>& v, float (&kl)[8],
+                       float (&kh)[8], float (&vl)[8], float (&vh)[8]) {
+    values8(k.lo, kl);
+    values8(k.hi, kh);
+    values8(v.lo, vl);
+    values8(v.hi, vh);
     if (a.w_k) unit_norm<HD>(kl, kh, a.w_k, c, a.eps);
     if (a.v_unit_norm) unit_norm<HD>(vl, vh, nullptr, c, a.eps);
-    if (on) {
+    if (written(slot)) {
       if (BIG) load_turn<HD>(s_turn, slot, c, cs, sn);
       rotate(kl, kh, cs, sn);
     }
@@ -228,11 +262,15 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
       }
     }
     for (int slot = slot0; slot < ps; slot += rstep) {
-      kv_rows(kv, slot, kl, kh, vl, vh);
-      m[0] = top_of(kl, kh, m[0]);
-      m[1] = top_of(vl, vh, m[1]);
+      if (BIG) load_kv(kv, slot, rk, rv);
+      kv_values(slot, rk, rv, kl, kh, vl, vh);
+      if (written(slot)) {
+        m[0] = top_of(kl, kh, m[0]);
+        m[1] = top_of(vl, vh, m[1]);
+      }
       if (!BIG) break;
     }
+    if (!BIG) load_kv(kv + 1, slot0, rk, rv);  // the next head's, while this one is coded
     float* sm = &s_max[kv & 1][0][0];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -256,9 +294,12 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
       if (threadIdx.x == 0) (t == 0 ? p.k_scales : p.v_scales)[pg] = sc;
     }
     for (int slot = slot0; slot < ps; slot += rstep) {
-      if (BIG) kv_rows(kv, slot, kl, kh, vl, vh);
+      if (BIG) {
+        load_kv(kv, slot, rk, rv);
+        kv_values(slot, rk, rv, kl, kh, vl, vh);
+      }
       const size_t at = base + (size_t)slot * HD + 8 * c;
-      if (slot >= first && slot < last) {
+      if (written(slot)) {
         *reinterpret_cast<uint2*>(p.k_codes + at) = codes8(kl, inv[0]);
         *reinterpret_cast<uint2*>(p.k_codes + at + HD / 2) = codes8(kh, inv[0]);
         *reinterpret_cast<uint2*>(p.v_codes + at) = codes8(vl, inv[1]);
@@ -278,29 +319,30 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
       }
       if (!BIG) break;
     }
-    if (a.q) {
-      for (int g = 0; g < G; ++g) {
-        const int h = kv * G + g;
-        for (int slot = slot0; slot < ps; slot += rstep) {
-          const bool on = slot >= first && slot < last;
-          float ql[8] = {}, qh[8] = {};
-          if (on) {
-            const T* qp = (const T*)a.q + (tok0 + slot) * a.q_stride + h * HD + 8 * c;
-            load8(qp, ql);
-            load8(qp + HD / 2, qh);
-          }
-          if (a.w_q) unit_norm<HD>(ql, qh, a.w_q, c, a.eps);
-          if (on) {
-            if (BIG) load_turn<HD>(s_turn, slot, c, cs, sn);
-            rotate(ql, qh, cs, sn);
-            T* op = (T*)a.q_out + ((tok0 + slot) * p.nh + h) * HD + 8 * c;
-            store8(op, ql);
-            store8(op + HD / 2, qh);
-          }
-          if (!BIG) break;
+  }
+  if (!a.q) return;
+  for (int slot = slot0; slot < ps; slot += rstep) {
+    const bool on = written(slot);
+    if (BIG && on) load_turn<HD>(s_turn, slot, c, cs, sn);
+    for (int h = q0; h < q1; h += QC) {
+      RawUnit<T> rq[QC];
+      load_q(h, slot, rq);
+#pragma unroll
+      for (int i = 0; i < QC; ++i) {
+        if (h + i >= q1) break;
+        float ql[8], qh[8];
+        values8(rq[i].lo, ql);
+        values8(rq[i].hi, qh);
+        if (a.w_q) unit_norm<HD>(ql, qh, a.w_q, c, a.eps);
+        if (on) {
+          rotate(ql, qh, cs, sn);
+          T* op = (T*)a.q_out + ((tok0 + slot) * p.nh + h + i) * HD + 8 * c;
+          store8(op, ql);
+          store8(op + HD / 2, qh);
         }
       }
     }
+    if (!BIG) break;
   }
 }
 
