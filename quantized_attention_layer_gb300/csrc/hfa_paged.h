@@ -29,11 +29,13 @@ struct PagedAppendArgs {
   const int* start;     // [batch]
   int total;            // rows of the packed arrays (bounds the rows cu may name)
   int single;           // every sequence has at most one row
-  int kv_per_cta;       // KV heads one CTA walks
+  // a page's CTAs: kv_groups of kv_per_cta K and V heads, then groups of q_per_cta query heads
+  int kv_groups, kv_per_cta, q_per_cta;
   const void *q, *k, *v;  // q nullable
   long long q_stride, k_stride, v_stride;  // elements
   void* q_out;
   const float2* rope_g;  // [hd/2] (hi, lo) of theta^(-2i/hd) / (2 pi) / f_i
+  const float4* slot_turn;  // [ps][hd/4] (cos, sin) of pairs 2i and 2i + 1 at positions 0 .. ps - 1
   const float* w_q;     // nullable [hd]
   const float* w_k;
   int v_unit_norm;

@@ -16,9 +16,10 @@ struct hfa_paged {
   hfa_paged_desc d;
   int device = 0, num_sms = 0;
   int ps_log2 = 0;
-  void* block = nullptr;  // error word, RoPE table, norm weights
+  void* block = nullptr;  // error word, RoPE table, norm weights, the slots' turns
   unsigned* err = nullptr;
   float2* rope_g = nullptr;
+  float4* slot_turn = nullptr;
   float* w_q = nullptr;
   float* w_k = nullptr;
   char msg[512] = {0};
@@ -208,15 +209,28 @@ extern "C" hfa_status hfa_paged_create(const hfa_paged_desc* desc, const float* 
   p->device = dev;
   p->num_sms = sms;
   while ((1 << p->ps_log2) < desc->page_size) ++p->ps_log2;
-  // one allocation: 256 bytes of error word, then the table and the weights
-  float host[256 + 2 * 256] = {0};
-  for (int i = 0; i < hd / 2; ++i) {
+  // one allocation: 256 bytes of error word, the frequencies and the weights (256 floats each),
+  // then the cosines and sines of positions 0 .. page_size - 1
+  const int half = hd / 2;
+  std::vector<float> host;
+  try {
+    host.resize(256 + (size_t)desc->page_size * hd);
+  } catch (const std::bad_alloc&) {
+    delete p;
+    return fail(nullptr, HFA_ENOMEM, "host memory");
+  }
+  for (int i = 0; i < half; ++i) {
     double v = pow((double)desc->rope_theta, -2.0 * i / hd) / (2.0 * M_PI);
     if (factors) v /= (double)factors[i];
     host[2 * i] = (float)v;
     host[2 * i + 1] = (float)(v - (double)host[2 * i]);
+    for (int s = 0; s < desc->page_size; ++s) {
+      const double turns = s * v, part = 2.0 * M_PI * (turns - floor(turns));
+      host[256 + ((size_t)s * half + i) * 2] = (float)cos(part);
+      host[256 + ((size_t)s * half + i) * 2 + 1] = (float)sin(part);
+    }
   }
-  const size_t bytes = 256 + 3 * 256 * sizeof(float);
+  const size_t bytes = 256 + (3 * 256 + (size_t)desc->page_size * hd) * sizeof(float);
   e = cudaMalloc(&p->block, bytes);
   if (e != cudaSuccess) {
     delete p;
@@ -227,9 +241,13 @@ extern "C" hfa_status hfa_paged_create(const hfa_paged_desc* desc, const float* 
   p->rope_g = (float2*)f;
   p->w_q = w_q ? f + 256 : nullptr;
   p->w_k = w_k ? f + 512 : nullptr;
+  p->slot_turn = (float4*)(f + 768);
   cudaStream_t s = (cudaStream_t)stream;
   e = cudaMemsetAsync(p->block, 0, bytes, s);
-  if (e == cudaSuccess) e = cudaMemcpyAsync(f, host, hd * sizeof(float), cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess) e = cudaMemcpyAsync(f, host.data(), hd * sizeof(float), cudaMemcpyHostToDevice, s);
+  if (e == cudaSuccess)
+    e = cudaMemcpyAsync(p->slot_turn, host.data() + 256, (size_t)desc->page_size * hd * sizeof(float),
+                        cudaMemcpyHostToDevice, s);
   if (e == cudaSuccess && w_q) e = cudaMemcpyAsync(p->w_q, w_q, hd * sizeof(float), cudaMemcpyDeviceToDevice, s);
   if (e == cudaSuccess && w_k) e = cudaMemcpyAsync(p->w_k, w_k, hd * sizeof(float), cudaMemcpyDeviceToDevice, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
@@ -318,6 +336,7 @@ extern "C" hfa_status hfa_paged_append(hfa_paged* p, void* stream, int batch, co
   a.v_stride = v_stride;
   a.q_out = q_out;
   a.rope_g = p->rope_g;
+  a.slot_turn = p->slot_turn;
   a.w_q = p->w_q;
   a.w_k = p->w_k;
   a.v_unit_norm = (d.flags & HFA_F_V_UNIT_NORM) != 0;

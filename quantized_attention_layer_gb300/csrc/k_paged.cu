@@ -19,7 +19,7 @@
 namespace hfa {
 namespace {
 
-constexpr int kAppendThreads = 512;  // most threads of an append CTA
+constexpr int kAppendThreads = 256;  // most threads of an append CTA
 
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p));
@@ -31,7 +31,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = pack_bf2(__float2bfloat16_rn(v[2 * i]), __float2bfloat16_rn(v[2 * i + 1]));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
@@ -77,18 +77,36 @@ __device__ __forceinline__ float finite_abs(float x) {
   const float a = fabsf(x);
   return a <= 3.402823466e38f ? a : 0.f;
 }
+// the larger magnitude, NaN if there is one
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
 // code of y under 1 / scale: ties to even, infinities to +-127, NaN to 0
 __device__ __forceinline__ uint32_t code_of(float y, float inv) {
   float t = y * inv;
   t = t == t ? fminf(fmaxf(t, -127.f), 127.f) : 0.f;
   return (uint32_t)__float2int_rn(t) & 0xffu;
 }
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], float inv) {
+// Codes of 8 values.  Finite ones are at most 127 (1 + 3 * 2^-24) scales: adding 1.5 * 2^23
+// rounds them to the nearest integer, ties to even, whose low byte is the code.
+__device__ __forceinline__ uint2 codes8(const float (&y)[8], float inv, bool finite) {
   uint32_t w[2];
+  if (finite) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-    w[h] = code_of(y[4 * h], inv) | code_of(y[4 * h + 1], inv) << 8 |
-           code_of(y[4 * h + 2], inv) << 16 | code_of(y[4 * h + 3], inv) << 24;
+    for (int h = 0; h < 2; ++h) {
+      uint32_t u[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(fmaf(y[4 * h + i], inv, 12582912.f));
+      w[h] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      w[h] = code_of(y[4 * h], inv) | code_of(y[4 * h + 1], inv) << 8 |
+             code_of(y[4 * h + 2], inv) << 16 | code_of(y[4 * h + 3], inv) << 24;
+  }
   return make_uint2(w[0], w[1]);
 }
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float r) {
@@ -101,60 +119,67 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float r) {
   return o;
 }
 
-// One row unit (16 values: lo the 8 at 8 c, hi the 8 at hd/2 + 8 c): RMS norm over the row,
-// whose HD / 16 units sit in adjacent lanes, times the weight (NULL: 1).
+// 1 / rms of a row, whose HD / 16 units (16 values: lo the 8 at 8 c, hi the 8 at hd/2 + 8 c)
+// sit in adjacent lanes.
 template <int HD>
-__device__ __forceinline__ void unit_norm(float (&lo)[8], float (&hi)[8], const float* w, int c,
-                                          float eps) {
+__device__ __forceinline__ float row_rms(const float (&lo)[8], const float (&hi)[8], float eps) {
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) ss += lo[i] * lo[i] + hi[i] * hi[i];
 #pragma unroll
   for (int o = 1; o < HD / 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float inv = rsqrtf(ss / HD + eps);
+  return rsqrtf(ss / HD + eps);
+}
+// The rotation of a unit's pairs with the norm's weights folded in:
+// (lo, hi) -> (lo w_lo cos - hi w_hi sin, lo w_lo sin + hi w_hi cos).
+struct Turn {
+  float a[8], b[8], c[8], d[8];
+};
+__device__ __forceinline__ void make_turn(Turn& t, const float (&cs)[8], const float (&sn)[8],
+                                          const float* w, int c, int half) {
   float wl[8], wh[8];
   if (w) {
     load8(w + 8 * c, wl);
-    load8(w + HD / 2 + 8 * c, wh);
+    load8(w + half + 8 * c, wh);
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    lo[i] *= w ? inv * wl[i] : inv;
-    hi[i] *= w ? inv * wh[i] : inv;
+    t.a[i] = w ? wl[i] * cs[i] : cs[i];
+    t.b[i] = w ? wh[i] * sn[i] : sn[i];
+    t.c[i] = w ? wl[i] * sn[i] : sn[i];
+    t.d[i] = w ? wh[i] * cs[i] : cs[i];
   }
 }
-__device__ __forceinline__ void rotate(float (&lo)[8], float (&hi)[8], const float (&cs)[8],
-                                       const float (&sn)[8]) {
+__device__ __forceinline__ void rotate(float (&lo)[8], float (&hi)[8], const Turn& t, bool norm,
+                                       float inv) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const float x0 = lo[i], x1 = hi[i];
-    lo[i] = x0 * cs[i] - x1 * sn[i];
-    hi[i] = x0 * sn[i] + x1 * cs[i];
+    lo[i] = x0 * t.a[i] - x1 * t.b[i];
+    hi[i] = x0 * t.c[i] + x1 * t.d[i];
   }
-}
-
-// The cosines and sines of a CTA's page when its rows do not fit one unit a thread: float4
-// (cos, sin, cos, sin) of pairs 8 c + 2 i, 8 c + 2 i + 1 of slot s at index (4 s + i) U + c,
-// so that the lanes of a row read adjacent 16-byte words.
-template <int HD>
-__device__ __forceinline__ void load_turn(const float4* tab, int slot, int c, float (&cs)[8],
-                                          float (&sn)[8]) {
+  if (norm) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 t = tab[(4 * slot + i) * (HD / 16) + c];
-    cs[2 * i] = t.x, sn[2 * i] = t.y, cs[2 * i + 1] = t.z, sn[2 * i + 1] = t.w;
+    for (int i = 0; i < 8; ++i) {
+      lo[i] *= inv;
+      hi[i] *= inv;
+    }
   }
 }
 
-// BIG: the page's ps * HD / 16 row units exceed 512 threads (pages of 128 at hd 128, of 64 or
-// 128 at hd 256): the threads loop over them, the turns live in shared memory, and K and V
-// rows are read twice (the second time from L2), once for the maximum and once for the codes.
+// The cosine and sine of slot s of a page are those of the page's first position, formed once
+// per CTA, turned by s: (c0 cs - s0 ss, s0 cs + c0 ss) with a table of the slots' (cs, ss).
+// BIG: the page's ps * HD / 16 row units exceed 256 threads: the threads loop over them, and K
+// and V rows are read twice (the second time from L2), for the maximum and for the codes.
 template <int HD, bool BIG, class T>
-__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const PagedAppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, 2) paged_append_kernel(const PagedAppendArgs a) {
   constexpr int U = HD / 16;  // units of a row
-  extern __shared__ float4 s_turn[];
+  // (cos, sin) of pairs 8 c + 2 i, 8 c + 2 i + 1 at the page's first position: index i U + c
+  __shared__ float4 s_base[HD / 4];
   __shared__ int s_seq;
-  __shared__ float s_max[2][2][kAppendThreads / 32];  // [head parity][K, V][warp]
+  // [round of heads, modulo 3][K, V][warp]: a slot is written again only behind a barrier that
+  // follows its last read
+  __shared__ float s_max[3][2][kAppendThreads / 32];
   const PagedView& p = a.p;
   const int ps = p.ps;
   const int item = blockIdx.x;
@@ -183,9 +208,12 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
   const int first = max(start - page0, 0), last = min(start + n - page0, ps);
   const int c = threadIdx.x % U, slot0 = threadIdx.x / U;
   const int rstep = blockDim.x / U;
-  const int G = p.nh / p.nkv;
+  // the CTAs of a page: the first kv_groups take its K and V heads, the others query heads
+  const bool queries = (int)blockIdx.y >= a.kv_groups;
   const int kv0 = blockIdx.y * a.kv_per_cta;
-  const int kv1 = min(kv0 + a.kv_per_cta, p.nkv);
+  const int kv1 = queries ? 0 : min(kv0 + a.kv_per_cta, p.nkv);
+  const int q0 = queries ? ((int)blockIdx.y - a.kv_groups) * a.q_per_cta : 0;
+  const int q1 = queries ? min(q0 + a.q_per_cta, p.nh) : 0;
   const long long tok0 = (long long)row0 + page0 - start;  // row of slot 0
   const int warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
   auto written = [&](int slot) { return slot >= first && slot < last; };
@@ -196,27 +224,63 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
   };
   // QC query heads at a time: their loads are in flight together
   constexpr int QC = sizeof(T) == 2 ? 4 : 2;
-  const int q0 = kv0 * G, q1 = kv1 * G;
   auto load_q = [&](int h, int slot, RawUnit<T> (&q)[QC]) {
 #pragma unroll
     for (int i = 0; i < QC; ++i)
       load_raw((const T*)a.q + (tok0 + slot) * a.q_stride + (h + i) * HD + 8 * c, HD / 2,
-               a.q && written(slot) && h + i < q1, q[i]);
+               written(slot) && h + i < q1, q[i]);
   };
   RawUnit<T> rk, rv;
-  if (!BIG) load_kv(kv0, slot0, rk, rv);
+  if (!BIG && !queries) load_kv(kv0, slot0, rk, rv);
 
   float cs[8], sn[8];
-  for (int slot = slot0; slot < ps; slot += rstep) {
-    if (!written(slot)) continue;
+  for (int i = threadIdx.x; i < HD / 2; i += blockDim.x) {
+    float2 v;
+    rope_cs(page0, a.rope_g[i], v.x, v.y);
+    reinterpret_cast<float2*>(s_base)[2 * ((i % 8 / 2) * U + i / 8) + i % 2] = v;
+  }
+  __syncthreads();
+  auto turn_of = [&](int slot) {
+    const float4* tab = a.slot_turn + ((size_t)slot * U + c) * 4;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rope_cs(page0 + slot, a.rope_g[8 * c + i], cs[i], sn[i]);
-    if (BIG) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        s_turn[(4 * slot + i) * U + c] = make_float4(cs[2 * i], sn[2 * i], cs[2 * i + 1], sn[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) {
+      const float4 t = __ldg(tab + i), o = s_base[i * U + c];
+      cs[2 * i] = o.x * t.x - o.y * t.y;
+      sn[2 * i] = o.y * t.x + o.x * t.y;
+      cs[2 * i + 1] = o.z * t.z - o.w * t.w;
+      sn[2 * i + 1] = o.w * t.z + o.z * t.w;
     }
-  }  // a thread reads back only what it wrote itself: no barrier
+  };
+  Turn turn;
+  if (queries) {
+    for (int slot = slot0; slot < ps; slot += rstep) {
+      const bool on = written(slot);
+      RawUnit<T> rq[QC];
+      load_q(q0, slot, rq);
+      if (on) turn_of(slot);
+      make_turn(turn, cs, sn, a.w_q, c, HD / 2);
+      for (int h = q0; h < q1; h += QC) {
+        if (h > q0) load_q(h, slot, rq);
+#pragma unroll
+        for (int i = 0; i < QC; ++i) {
+          if (h + i >= q1) break;
+          float ql[8], qh[8];
+          values8(rq[i].lo, ql);
+          values8(rq[i].hi, qh);
+          const float inv = a.w_q ? row_rms<HD>(ql, qh, a.eps) : 1.f;
+          if (on) {
+            rotate(ql, qh, turn, a.w_q != nullptr, inv);
+            T* op = (T*)a.q_out + ((tok0 + slot) * p.nh + h + i) * HD + 8 * c;
+            store8(op, ql);
+            store8(op + HD / 2, qh);
+          }
+        }
+      }
+      if (!BIG) break;
+    }
+    return;
+  }
+  if (!BIG && written(slot0)) turn_of(slot0);
   if ((unsigned)page >= (unsigned)p.num_pages) {
     if (threadIdx.x == 0) atomicOr(p.err, kErrBadPosition);
     return;
@@ -224,22 +288,37 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
 
   // the K and V values of a unit, normed and rotated.  Every lane of a warp calls it together
   // (the norm's sum goes over the lanes of a row).
+  if (!BIG) make_turn(turn, cs, sn, a.w_k, c, HD / 2);
   auto kv_values = [&](int slot, const RawUnit<T>& k, const RawUnit<T>& v, float (&kl)[8],
                        float (&kh)[8], float (&vl)[8], float (&vh)[8]) {
     values8(k.lo, kl);
     values8(k.hi, kh);
     values8(v.lo, vl);
     values8(v.hi, vh);
-    if (a.w_k) unit_norm<HD>(kl, kh, a.w_k, c, a.eps);
-    if (a.v_unit_norm) unit_norm<HD>(vl, vh, nullptr, c, a.eps);
+    const float inv = a.w_k ? row_rms<HD>(kl, kh, a.eps) : 1.f;
+    if (a.v_unit_norm) {
+      const float iv = row_rms<HD>(vl, vh, a.eps);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        vl[i] *= iv;
+        vh[i] *= iv;
+      }
+    }
     if (written(slot)) {
-      if (BIG) load_turn<HD>(s_turn, slot, c, cs, sn);
-      rotate(kl, kh, cs, sn);
+      if (BIG) {
+        turn_of(slot);
+        make_turn(turn, cs, sn, a.w_k, c, HD / 2);
+      }
+      rotate(kl, kh, turn, a.w_k != nullptr, inv);
     }
   };
-  auto top_of = [&](const float (&lo)[8], const float (&hi)[8], float m) {
+  // the largest magnitude so far: NaN or infinite once a value is not finite, or over the
+  // finite ones alone
+  auto top_of = [&](const float (&lo)[8], const float (&hi)[8], float m, bool all) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(finite_abs(lo[i]), finite_abs(hi[i])));
+    for (int i = 0; i < 8; ++i)
+      m = all ? max_nan(m, max_nan(fabsf(lo[i]), fabsf(hi[i])))
+              : fmaxf(m, fmaxf(finite_abs(lo[i]), finite_abs(hi[i])));
     return m;
   };
 
@@ -249,7 +328,6 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
     float kl[8], kh[8], vl[8], vh[8];
     uint2 old[4];
     float s_old[2] = {0.f, 0.f};
-    float m[2] = {0.f, 0.f};
     if (first > 0) {
       s_old[0] = p.k_scales[pg];
       s_old[1] = p.v_scales[pg];
@@ -261,32 +339,43 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
         old[3] = *reinterpret_cast<const uint2*>(p.v_codes + at + HD / 2);
       }
     }
-    for (int slot = slot0; slot < ps; slot += rstep) {
-      if (BIG) load_kv(kv, slot, rk, rv);
-      kv_values(slot, rk, rv, kl, kh, vl, vh);
-      if (written(slot)) {
-        m[0] = top_of(kl, kh, m[0]);
-        m[1] = top_of(vl, vh, m[1]);
+    // the page's maxima; a block that holds something not finite looks again at the rest
+    float tops[2];
+    bool finite = true;
+    for (int round = 0; round < 2; ++round) {
+      float m[2] = {0.f, 0.f};
+      for (int slot = slot0; slot < ps; slot += rstep) {
+        if (BIG) load_kv(kv, slot, rk, rv);
+        if (BIG || round == 0) kv_values(slot, rk, rv, kl, kh, vl, vh);
+        if (written(slot)) {
+          m[0] = top_of(kl, kh, m[0], round == 0);
+          m[1] = top_of(vl, vh, m[1], round == 0);
+        }
+        if (!BIG) break;
       }
-      if (!BIG) break;
-    }
-    if (!BIG) load_kv(kv + 1, slot0, rk, rv);  // the next head's, while this one is coded
-    float* sm = &s_max[kv & 1][0][0];
+      if (!BIG && round == 0) load_kv(kv + 1, slot0, rk, rv);  // the next head's, while this one is coded
+      float* sm = &s_max[(2 * kv + round) % 3][0][0];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < 2; ++t) {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m[t] = fmaxf(m[t], __shfl_xor_sync(0xffffffffu, m[t], o));
-      if ((threadIdx.x & 31) == 0) sm[t * (kAppendThreads / 32) + warp] = m[t];
+        for (int o = 16; o > 0; o >>= 1) m[t] = max_nan(m[t], __shfl_xor_sync(0xffffffffu, m[t], o));
+        if ((threadIdx.x & 31) == 0) sm[t * (kAppendThreads / 32) + warp] = m[t];
+      }
+      __syncthreads();  // also: every thread has read the old scales
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        tops[t] = 0.f;
+        for (int w = 0; w < nwarps; ++w) tops[t] = max_nan(tops[t], sm[t * (kAppendThreads / 32) + w]);
+      }
+      if (round == 0 && tops[0] <= 3.402823466e38f && tops[1] <= 3.402823466e38f) break;
+      finite = false;
     }
-    __syncthreads();  // also: every thread has read the old scales
     float inv[2], ratio[2];
     bool grown[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      float top = 0.f;
-      for (int w = 0; w < nwarps; ++w) top = fmaxf(top, sm[t * (kAppendThreads / 32) + w]);
       const float so = s_old[t] > 0.f ? finite_abs(s_old[t]) : 0.f;
-      float sc = fmaxf(so, top / 127.f);
+      float sc = fmaxf(so, tops[t] / 127.f);
       if (sc < 1.17549435e-38f) sc = 0.f;
       inv[t] = sc > 0.f ? 1.f / sc : 0.f;
       ratio[t] = sc > 0.f ? so / sc : 0.f;
@@ -300,10 +389,10 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
       }
       const size_t at = base + (size_t)slot * HD + 8 * c;
       if (written(slot)) {
-        *reinterpret_cast<uint2*>(p.k_codes + at) = codes8(kl, inv[0]);
-        *reinterpret_cast<uint2*>(p.k_codes + at + HD / 2) = codes8(kh, inv[0]);
-        *reinterpret_cast<uint2*>(p.v_codes + at) = codes8(vl, inv[1]);
-        *reinterpret_cast<uint2*>(p.v_codes + at + HD / 2) = codes8(vh, inv[1]);
+        *reinterpret_cast<uint2*>(p.k_codes + at) = codes8(kl, inv[0], finite);
+        *reinterpret_cast<uint2*>(p.k_codes + at + HD / 2) = codes8(kh, inv[0], finite);
+        *reinterpret_cast<uint2*>(p.v_codes + at) = codes8(vl, inv[1], finite);
+        *reinterpret_cast<uint2*>(p.v_codes + at + HD / 2) = codes8(vh, inv[1], finite);
       } else if (slot < first) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -320,47 +409,19 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
       if (!BIG) break;
     }
   }
-  if (!a.q) return;
-  for (int slot = slot0; slot < ps; slot += rstep) {
-    const bool on = written(slot);
-    if (BIG && on) load_turn<HD>(s_turn, slot, c, cs, sn);
-    for (int h = q0; h < q1; h += QC) {
-      RawUnit<T> rq[QC];
-      load_q(h, slot, rq);
-#pragma unroll
-      for (int i = 0; i < QC; ++i) {
-        if (h + i >= q1) break;
-        float ql[8], qh[8];
-        values8(rq[i].lo, ql);
-        values8(rq[i].hi, qh);
-        if (a.w_q) unit_norm<HD>(ql, qh, a.w_q, c, a.eps);
-        if (on) {
-          rotate(ql, qh, cs, sn);
-          T* op = (T*)a.q_out + ((tok0 + slot) * p.nh + h + i) * HD + 8 * c;
-          store8(op, ql);
-          store8(op + HD / 2, qh);
-        }
-      }
-    }
-    if (!BIG) break;
-  }
 }
 
 template <int HD, bool BIG, class T>
 cudaError_t launch_append(const PagedAppendArgs& a, dim3 grid, int threads, cudaStream_t s) {
-  const size_t smem = BIG ? (size_t)a.p.ps * HD * 4 : 0;  // ps * (HD / 16) * 4 float4
-  if (BIG) {
-    const cudaError_t e = cudaFuncSetAttribute(paged_append_kernel<HD, BIG, T>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
-  paged_append_kernel<HD, BIG, T><<<grid, threads, smem, s>>>(a);
+  paged_append_kernel<HD, BIG, T><<<grid, threads, 0, s>>>(a);
   return cudaGetLastError();
 }
 template <class T>
 cudaError_t launch_append_t(const PagedAppendArgs& a, dim3 grid, int threads, bool big,
                             cudaStream_t s) {
-  if (a.p.hd == 64) return launch_append<64, false, T>(a, grid, threads, s);
+  if (a.p.hd == 64)
+    return big ? launch_append<64, true, T>(a, grid, threads, s)
+               : launch_append<64, false, T>(a, grid, threads, s);
   if (a.p.hd == 128)
     return big ? launch_append<128, true, T>(a, grid, threads, s)
                : launch_append<128, false, T>(a, grid, threads, s);
@@ -425,12 +486,16 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a0, bool f32, int items, 
   PagedAppendArgs a = a0;
   const int units = a.p.ps * (a.p.hd / 16);
   const int threads = units < kAppendThreads ? units : kAppendThreads;
-  // KV heads per CTA: as many as leave every SM eight CTAs (the position's cosines and sines
-  // are computed once per CTA)
-  int per = 1;
-  while (per < a.p.nkv && (long long)items * ((a.p.nkv + 2 * per - 1) / (2 * per)) >= 8LL * sms) per *= 2;
+  // Heads per CTA: as many as leave every SM eight CTAs (the turns of its rows are formed once
+  // per CTA), the query heads in steps of the four whose loads are in flight together
+  auto groups = [&](int heads, int per) { return (heads + per - 1) / per; };
+  int per = 1, qper = 4;
+  while (per < a.p.nkv && (long long)items * groups(a.p.nkv, 2 * per) >= 8LL * sms) per *= 2;
+  while (qper < a.p.nh && (long long)items * groups(a.p.nh, 2 * qper) >= 4LL * sms) qper *= 2;
   a.kv_per_cta = per;
-  const dim3 grid(items, (a.p.nkv + per - 1) / per);
+  a.q_per_cta = qper;
+  a.kv_groups = groups(a.p.nkv, per);
+  const dim3 grid(items, a.kv_groups + (a.q ? groups(a.p.nh, qper) : 0));
   const bool big = units > threads;
   return f32 ? launch_append_t<float>(a, grid, threads, big, s)
              : launch_append_t<__nv_bfloat16>(a, grid, threads, big, s);
