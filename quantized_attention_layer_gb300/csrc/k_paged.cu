@@ -7,10 +7,12 @@
 //   s' = max(s, a / 127), s the page's scale or 0 for a page begun by this call,
 //   codes before the first written slot: rint(c (s / s')), written ones: rint(y / s').
 // One CTA owns a (sequence, page) and walks over some KV heads, so the maximum of a page
-// meets in one block and nothing is atomic: results do not depend on timing.  A thread holds
-// 16 values of a row, 8 of each half, so both members of its pairs are its own and the
-// cosines and sines of its position, computed once, serve every q and k head of the walk.
-// Memory-bound: rows are read once with 16-byte loads and codes written once.
+// meets in one block and nothing is atomic: results do not depend on timing.  Other CTAs of
+// the page rotate the queries, four heads' loads in flight together.  A thread holds 8 values
+// of a row, 4 of each half, so both members of its pairs are its own, and few registers: four
+// CTAs of 256 threads share an SM, one loading while another computes (with 16 values a thread
+// and 16 warps an SM an 8K prompt took 53 us).  Memory-bound by design; the issue slots come
+// next (about 20 instructions a value).
 #include "hfa_common.cuh"
 #include "hfa_finish.cuh"
 #include "hfa_internal.h"
@@ -21,55 +23,50 @@ namespace {
 
 constexpr int kAppendThreads = 256;  // most threads of an append CTA
 
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
   const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  uint32_t w[4];
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
+  uint32_t w[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 
-// A row unit as it lies in memory (8 values of each half), and as values.
+// A row unit: 4 values of each half as they lie in memory.  Plain loads: the queries may be
+// overwritten in place.
 template <class T>
-struct RawUnit {
-  static constexpr int W = sizeof(T) * 8 / 16;  // 16-byte words of 8 values
-  uint4 lo[W], hi[W];
+struct RawUnit;
+template <>
+struct RawUnit<__nv_bfloat16> {
+  using Word = uint2;
+  Word lo, hi;
+};
+template <>
+struct RawUnit<float> {
+  using Word = float4;
+  Word lo, hi;
 };
 template <class T>
 __device__ __forceinline__ void load_raw(const T* p, int half, bool on, RawUnit<T>& u) {
-#pragma unroll
-  for (int i = 0; i < RawUnit<T>::W; ++i) {
-    u.lo[i] = u.hi[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (on) {
-      // plain loads: the queries may be overwritten in place
-      u.lo[i] = reinterpret_cast<const uint4*>(p)[i];
-      u.hi[i] = reinterpret_cast<const uint4*>(p + half)[i];
-    }
+  using Word = typename RawUnit<T>::Word;
+  u.lo = u.hi = Word{};
+  if (on) {
+    u.lo = *reinterpret_cast<const Word*>(p);
+    u.hi = *reinterpret_cast<const Word*>(p + half);
   }
 }
-__device__ __forceinline__ void values8(const uint4 (&r)[1], float (&v)[8]) {
-  const uint32_t w[4] = {r[0].x, r[0].y, r[0].z, r[0].w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+__device__ __forceinline__ void values4(uint2 r, float (&v)[4]) {
+  v[0] = __uint_as_float(r.x << 16), v[1] = __uint_as_float(r.x & 0xffff0000u);
+  v[2] = __uint_as_float(r.y << 16), v[3] = __uint_as_float(r.y & 0xffff0000u);
 }
-__device__ __forceinline__ void values8(const uint4 (&r)[2], float (&v)[8]) {
-  v[0] = __uint_as_float(r[0].x), v[1] = __uint_as_float(r[0].y);
-  v[2] = __uint_as_float(r[0].z), v[3] = __uint_as_float(r[0].w);
-  v[4] = __uint_as_float(r[1].x), v[5] = __uint_as_float(r[1].y);
-  v[6] = __uint_as_float(r[1].z), v[7] = __uint_as_float(r[1].w);
+__device__ __forceinline__ void values4(float4 r, float (&v)[4]) {
+  v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
 }
 
 // |x| for finite x, 0 for NaN and infinities
@@ -89,25 +86,16 @@ __device__ __forceinline__ uint32_t code_of(float y, float inv) {
   t = t == t ? fminf(fmaxf(t, -127.f), 127.f) : 0.f;
   return (uint32_t)__float2int_rn(t) & 0xffu;
 }
-// Codes of 8 values.  Finite ones are at most 127 (1 + 3 * 2^-24) scales: adding 1.5 * 2^23
+// Codes of 4 values.  Finite ones are at most 127 (1 + 3 * 2^-24) scales: adding 1.5 * 2^23
 // rounds them to the nearest integer, ties to even, whose low byte is the code.
-__device__ __forceinline__ uint2 codes8(const float (&y)[8], float inv, bool finite) {
-  uint32_t w[2];
+__device__ __forceinline__ uint32_t codes4(const float (&y)[4], float inv, bool finite) {
   if (finite) {
+    uint32_t u[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      uint32_t u[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(fmaf(y[4 * h + i], inv, 12582912.f));
-      w[h] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
-    }
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      w[h] = code_of(y[4 * h], inv) | code_of(y[4 * h + 1], inv) << 8 |
-             code_of(y[4 * h + 2], inv) << 16 | code_of(y[4 * h + 3], inv) << 24;
+    for (int i = 0; i < 4; ++i) u[i] = __float_as_uint(fmaf(y[i], inv, 12582912.f));
+    return __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
   }
-  return make_uint2(w[0], w[1]);
+  return code_of(y[0], inv) | code_of(y[1], inv) << 8 | code_of(y[2], inv) << 16 | code_of(y[3], inv) << 24;
 }
 __device__ __forceinline__ uint32_t recode4(uint32_t w, float r) {
   uint32_t o = 0;
@@ -119,48 +107,48 @@ __device__ __forceinline__ uint32_t recode4(uint32_t w, float r) {
   return o;
 }
 
-// 1 / rms of a row, whose HD / 16 units (16 values: lo the 8 at 8 c, hi the 8 at hd/2 + 8 c)
+// 1 / rms of a row, whose HD / 8 units (8 values: lo the 4 at 4 c, hi the 4 at hd/2 + 4 c)
 // sit in adjacent lanes.
 template <int HD>
-__device__ __forceinline__ float row_rms(const float (&lo)[8], const float (&hi)[8], float eps) {
+__device__ __forceinline__ float row_rms(const float (&lo)[4], const float (&hi)[4], float eps) {
   float ss = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss += lo[i] * lo[i] + hi[i] * hi[i];
+  for (int i = 0; i < 4; ++i) ss += lo[i] * lo[i] + hi[i] * hi[i];
 #pragma unroll
-  for (int o = 1; o < HD / 16; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+  for (int o = 1; o < HD / 8; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   return rsqrtf(ss / HD + eps);
 }
 // The rotation of a unit's pairs with the norm's weights folded in:
 // (lo, hi) -> (lo w_lo cos - hi w_hi sin, lo w_lo sin + hi w_hi cos).
 struct Turn {
-  float a[8], b[8], c[8], d[8];
+  float a[4], b[4], c[4], d[4];
 };
-__device__ __forceinline__ void make_turn(Turn& t, const float (&cs)[8], const float (&sn)[8],
+__device__ __forceinline__ void make_turn(Turn& t, const float (&cs)[4], const float (&sn)[4],
                                           const float* w, int c, int half) {
-  float wl[8], wh[8];
+  float wl[4], wh[4];
   if (w) {
-    load8(w + 8 * c, wl);
-    load8(w + half + 8 * c, wh);
+    load4(w + 4 * c, wl);
+    load4(w + half + 4 * c, wh);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     t.a[i] = w ? wl[i] * cs[i] : cs[i];
     t.b[i] = w ? wh[i] * sn[i] : sn[i];
     t.c[i] = w ? wl[i] * sn[i] : sn[i];
     t.d[i] = w ? wh[i] * cs[i] : cs[i];
   }
 }
-__device__ __forceinline__ void rotate(float (&lo)[8], float (&hi)[8], const Turn& t, bool norm,
+__device__ __forceinline__ void rotate(float (&lo)[4], float (&hi)[4], const Turn& t, bool norm,
                                        float inv) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const float x0 = lo[i], x1 = hi[i];
     lo[i] = x0 * t.a[i] - x1 * t.b[i];
     hi[i] = x0 * t.c[i] + x1 * t.d[i];
   }
   if (norm) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       lo[i] *= inv;
       hi[i] *= inv;
     }
@@ -169,12 +157,12 @@ __device__ __forceinline__ void rotate(float (&lo)[8], float (&hi)[8], const Tur
 
 // The cosine and sine of slot s of a page are those of the page's first position, formed once
 // per CTA, turned by s: (c0 cs - s0 ss, s0 cs + c0 ss) with a table of the slots' (cs, ss).
-// BIG: the page's ps * HD / 16 row units exceed 256 threads: the threads loop over them, and K
+// BIG: the page's ps * HD / 8 row units exceed 256 threads: the threads loop over them, and K
 // and V rows are read twice (the second time from L2), for the maximum and for the codes.
 template <int HD, bool BIG, class T>
-__global__ void __launch_bounds__(kAppendThreads, 2) paged_append_kernel(const PagedAppendArgs a) {
-  constexpr int U = HD / 16;  // units of a row
-  // (cos, sin) of pairs 8 c + 2 i, 8 c + 2 i + 1 at the page's first position: index i U + c
+__global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(const PagedAppendArgs a) {
+  constexpr int U = HD / 8;  // units of a row
+  // (cos, sin) of pairs 4 c + 2 i, 4 c + 2 i + 1 at the page's first position: index i U + c
   __shared__ float4 s_base[HD / 4];
   __shared__ int s_seq;
   // [round of heads, modulo 3][K, V][warp]: a slot is written again only behind a barrier that
@@ -219,31 +207,31 @@ __global__ void __launch_bounds__(kAppendThreads, 2) paged_append_kernel(const P
   auto written = [&](int slot) { return slot >= first && slot < last; };
   auto load_kv = [&](int kv, int slot, RawUnit<T>& k, RawUnit<T>& v) {
     const bool on = written(slot) && kv < kv1;
-    load_raw((const T*)a.k + (tok0 + slot) * a.k_stride + kv * HD + 8 * c, HD / 2, on, k);
-    load_raw((const T*)a.v + (tok0 + slot) * a.v_stride + kv * HD + 8 * c, HD / 2, on, v);
+    load_raw((const T*)a.k + (tok0 + slot) * a.k_stride + kv * HD + 4 * c, HD / 2, on, k);
+    load_raw((const T*)a.v + (tok0 + slot) * a.v_stride + kv * HD + 4 * c, HD / 2, on, v);
   };
   // QC query heads at a time: their loads are in flight together
   constexpr int QC = sizeof(T) == 2 ? 4 : 2;
   auto load_q = [&](int h, int slot, RawUnit<T> (&q)[QC]) {
 #pragma unroll
     for (int i = 0; i < QC; ++i)
-      load_raw((const T*)a.q + (tok0 + slot) * a.q_stride + (h + i) * HD + 8 * c, HD / 2,
+      load_raw((const T*)a.q + (tok0 + slot) * a.q_stride + (h + i) * HD + 4 * c, HD / 2,
                written(slot) && h + i < q1, q[i]);
   };
   RawUnit<T> rk, rv;
   if (!BIG && !queries) load_kv(kv0, slot0, rk, rv);
 
-  float cs[8], sn[8];
+  float cs[4], sn[4];
   for (int i = threadIdx.x; i < HD / 2; i += blockDim.x) {
     float2 v;
     rope_cs(page0, a.rope_g[i], v.x, v.y);
-    reinterpret_cast<float2*>(s_base)[2 * ((i % 8 / 2) * U + i / 8) + i % 2] = v;
+    reinterpret_cast<float2*>(s_base)[2 * ((i % 4 / 2) * U + i / 4) + i % 2] = v;
   }
   __syncthreads();
   auto turn_of = [&](int slot) {
-    const float4* tab = a.slot_turn + ((size_t)slot * U + c) * 4;
+    const float4* tab = a.slot_turn + ((size_t)slot * U + c) * 2;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const float4 t = __ldg(tab + i), o = s_base[i * U + c];
       cs[2 * i] = o.x * t.x - o.y * t.y;
       sn[2 * i] = o.y * t.x + o.x * t.y;
@@ -264,15 +252,15 @@ __global__ void __launch_bounds__(kAppendThreads, 2) paged_append_kernel(const P
 #pragma unroll
         for (int i = 0; i < QC; ++i) {
           if (h + i >= q1) break;
-          float ql[8], qh[8];
-          values8(rq[i].lo, ql);
-          values8(rq[i].hi, qh);
+          float ql[4], qh[4];
+          values4(rq[i].lo, ql);
+          values4(rq[i].hi, qh);
           const float inv = a.w_q ? row_rms<HD>(ql, qh, a.eps) : 1.f;
           if (on) {
             rotate(ql, qh, turn, a.w_q != nullptr, inv);
-            T* op = (T*)a.q_out + ((tok0 + slot) * p.nh + h + i) * HD + 8 * c;
-            store8(op, ql);
-            store8(op + HD / 2, qh);
+            T* op = (T*)a.q_out + ((tok0 + slot) * p.nh + h + i) * HD + 4 * c;
+            store4(op, ql);
+            store4(op + HD / 2, qh);
           }
         }
       }
@@ -289,17 +277,17 @@ __global__ void __launch_bounds__(kAppendThreads, 2) paged_append_kernel(const P
   // the K and V values of a unit, normed and rotated.  Every lane of a warp calls it together
   // (the norm's sum goes over the lanes of a row).
   if (!BIG) make_turn(turn, cs, sn, a.w_k, c, HD / 2);
-  auto kv_values = [&](int slot, const RawUnit<T>& k, const RawUnit<T>& v, float (&kl)[8],
-                       float (&kh)[8], float (&vl)[8], float (&vh)[8]) {
-    values8(k.lo, kl);
-    values8(k.hi, kh);
-    values8(v.lo, vl);
-    values8(v.hi, vh);
+  auto kv_values = [&](int slot, const RawUnit<T>& k, const RawUnit<T>& v, float (&kl)[4],
+                       float (&kh)[4], float (&vl)[4], float (&vh)[4]) {
+    values4(k.lo, kl);
+    values4(k.hi, kh);
+    values4(v.lo, vl);
+    values4(v.hi, vh);
     const float inv = a.w_k ? row_rms<HD>(kl, kh, a.eps) : 1.f;
     if (a.v_unit_norm) {
       const float iv = row_rms<HD>(vl, vh, a.eps);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         vl[i] *= iv;
         vh[i] *= iv;
       }
@@ -314,9 +302,9 @@ __global__ void __launch_bounds__(kAppendThreads, 2) paged_append_kernel(const P
   };
   // the largest magnitude so far: NaN or infinite once a value is not finite, or over the
   // finite ones alone
-  auto top_of = [&](const float (&lo)[8], const float (&hi)[8], float m, bool all) {
+  auto top_of = [&](const float (&lo)[4], const float (&hi)[4], float m, bool all) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
       m = all ? max_nan(m, max_nan(fabsf(lo[i]), fabsf(hi[i])))
               : fmaxf(m, fmaxf(finite_abs(lo[i]), finite_abs(hi[i])));
     return m;
@@ -325,18 +313,18 @@ __global__ void __launch_bounds__(kAppendThreads, 2) paged_append_kernel(const P
   for (int kv = kv0; kv < kv1; ++kv) {
     const size_t pg = (size_t)page * p.nkv + kv;
     const size_t base = pg * ps * HD;
-    float kl[8], kh[8], vl[8], vh[8];
-    uint2 old[4];
+    float kl[4], kh[4], vl[4], vh[4];
+    uint32_t old[4];
     float s_old[2] = {0.f, 0.f};
     if (first > 0) {
       s_old[0] = p.k_scales[pg];
       s_old[1] = p.v_scales[pg];
       if (!BIG && slot0 < first) {  // early: needed only if the scale grows
-        const size_t at = base + (size_t)slot0 * HD + 8 * c;
-        old[0] = *reinterpret_cast<const uint2*>(p.k_codes + at);
-        old[1] = *reinterpret_cast<const uint2*>(p.k_codes + at + HD / 2);
-        old[2] = *reinterpret_cast<const uint2*>(p.v_codes + at);
-        old[3] = *reinterpret_cast<const uint2*>(p.v_codes + at + HD / 2);
+        const size_t at = base + (size_t)slot0 * HD + 4 * c;
+        old[0] = *reinterpret_cast<const uint32_t*>(p.k_codes + at);
+        old[1] = *reinterpret_cast<const uint32_t*>(p.k_codes + at + HD / 2);
+        old[2] = *reinterpret_cast<const uint32_t*>(p.v_codes + at);
+        old[3] = *reinterpret_cast<const uint32_t*>(p.v_codes + at + HD / 2);
       }
     }
     // the page's maxima; a block that holds something not finite looks again at the rest
@@ -387,12 +375,12 @@ __global__ void __launch_bounds__(kAppendThreads, 2) paged_append_kernel(const P
         load_kv(kv, slot, rk, rv);
         kv_values(slot, rk, rv, kl, kh, vl, vh);
       }
-      const size_t at = base + (size_t)slot * HD + 8 * c;
+      const size_t at = base + (size_t)slot * HD + 4 * c;
       if (written(slot)) {
-        *reinterpret_cast<uint2*>(p.k_codes + at) = codes8(kl, inv[0], finite);
-        *reinterpret_cast<uint2*>(p.k_codes + at + HD / 2) = codes8(kh, inv[0], finite);
-        *reinterpret_cast<uint2*>(p.v_codes + at) = codes8(vl, inv[1], finite);
-        *reinterpret_cast<uint2*>(p.v_codes + at + HD / 2) = codes8(vh, inv[1], finite);
+        *reinterpret_cast<uint32_t*>(p.k_codes + at) = codes4(kl, inv[0], finite);
+        *reinterpret_cast<uint32_t*>(p.k_codes + at + HD / 2) = codes4(kh, inv[0], finite);
+        *reinterpret_cast<uint32_t*>(p.v_codes + at) = codes4(vl, inv[1], finite);
+        *reinterpret_cast<uint32_t*>(p.v_codes + at + HD / 2) = codes4(vh, inv[1], finite);
       } else if (slot < first) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -400,9 +388,8 @@ __global__ void __launch_bounds__(kAppendThreads, 2) paged_append_kernel(const P
           int8_t* dst = (t == 0 ? p.k_codes : p.v_codes) + at;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            uint2* at8 = reinterpret_cast<uint2*>(dst + h * (HD / 2));
-            const uint2 w = BIG ? *at8 : old[2 * t + h];
-            *at8 = make_uint2(recode4(w.x, ratio[t]), recode4(w.y, ratio[t]));
+            uint32_t* at4 = reinterpret_cast<uint32_t*>(dst + h * (HD / 2));
+            *at4 = recode4(BIG ? *at4 : old[2 * t + h], ratio[t]);
           }
         }
       }
@@ -484,7 +471,7 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const PagedReadArgs a) 
 cudaError_t launch_paged_append(const PagedAppendArgs& a0, bool f32, int items, int sms,
                                 cudaStream_t s) {
   PagedAppendArgs a = a0;
-  const int units = a.p.ps * (a.p.hd / 16);
+  const int units = a.p.ps * (a.p.hd / 8);
   const int threads = units < kAppendThreads ? units : kAppendThreads;
   // Heads per CTA: as many as leave every SM eight CTAs (the turns of its rows are formed once
   // per CTA), the query heads in steps of the four whose loads are in flight together
