@@ -416,19 +416,21 @@ cudaError_t launch_append_t(const PagedAppendArgs& a, dim3 grid, int threads, bo
              : launch_append<256, false, T>(a, grid, threads, s);
 }
 
-// Read: one CTA decodes one page's rows of some KV heads, 16 codes (one 16-byte load, two
-// 16-byte stores) a thread and step; memory-bound.
+// Read: one CTA decodes one page's rows of some KV heads; a thread takes the 8 codes of chunk
+// c of rows r, r + 256 / U, ...: one 8-byte load and one 16-byte store each, so that a warp's
+// store is 512 whole bytes, four rows' loads in flight.  Memory-bound.
+template <int HD>
 __global__ void __launch_bounds__(256) paged_read_kernel(const PagedReadArgs a) {
+  constexpr int U = HD / 8, RP = 256 / U, NB = 4;
   const PagedView& p = a.p;
   const int b = blockIdx.y;
   const int start = a.start[b], n = a.count[b];
   if (n <= 0) return;
-  if (start < 0 || start + (long long)n > (long long)p.max_pages * p.ps ||
-      start + (long long)n > a.capacity) {
+  if (start < 0 || start > p.max_pages * p.ps - n || start > a.capacity - n) {
     if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(p.err, kErrBadPosition);
     return;
   }
-  const int U = p.hd / 16;
+  const int c = threadIdx.x % U, r0 = threadIdx.x / U;
   const int kv0 = blockIdx.z * a.heads_per_cta;
   const int heads = min(a.heads_per_cta, p.nkv - kv0);
   const int jend = (start + n - 1) >> p.ps_log2;
@@ -440,28 +442,40 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const PagedReadArgs a) 
     }
     const int page0 = j << p.ps_log2;
     const int first = max(start - page0, 0), last = min(start + n - page0, p.ps);
-    const int per = (last - first) * U;  // units of one head's rows
-#pragma unroll 4
-    for (int i = threadIdx.x; i < 2 * heads * per; i += blockDim.x) {
-      const int hu = i / per, u = i - hu * per;
-      const int t = hu >= heads, kv = kv0 + hu - t * heads;
-      const int slot = first + u / U, c = u % U;
-      const size_t pg = (size_t)page * p.nkv + kv;
-      const int8_t* codes = t ? p.v_codes : p.k_codes;
-      const float sc = __ldg((t ? p.v_scales : p.k_scales) + pg);
-      const uint4 w4 = __ldg(reinterpret_cast<const uint4*>(codes + (pg * p.ps + slot) * p.hd) + c);
-      const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-      uint32_t o[8];
+    const int blocks = (last - first + RP - 1) / RP;  // row blocks of one head
+    const int steps = 2 * heads * blocks;
+    for (int s0 = 0; s0 < steps; s0 += NB) {
+      uint2 w[NB];
+      float sc[NB];
+      size_t at[NB];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int s0 = 16 * (q & 1);
-        o[q] = pack_bf2(__float2bfloat16_rn((float)(int8_t)(w[q >> 1] >> s0) * sc),
-                        __float2bfloat16_rn((float)(int8_t)(w[q >> 1] >> (s0 + 8)) * sc));
+      for (int x = 0; x < NB; ++x) {
+        const int hu = (s0 + x) / blocks, slot = first + (s0 + x - hu * blocks) * RP + r0;
+        const int t = hu >= heads, kv = kv0 + hu - t * heads;
+        const bool on = s0 + x < steps && slot < last;
+        at[x] = (size_t)-1;
+        if (on) {
+          const size_t pg = (size_t)page * p.nkv + kv;
+          sc[x] = __ldg((t ? p.v_scales : p.k_scales) + pg);
+          w[x] = __ldg(reinterpret_cast<const uint2*>((t ? p.v_codes : p.k_codes) + (pg * p.ps + slot) * HD) + c);
+          at[x] = (((size_t)b * p.nkv + kv) * a.capacity + page0 + slot) * HD + 8 * c;
+        }
       }
-      __nv_bfloat16* dst = (t ? a.v_cache : a.k_cache) +
-                           (((size_t)b * p.nkv + kv) * a.capacity + page0 + slot) * p.hd + 16 * c;
-      reinterpret_cast<uint4*>(dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      reinterpret_cast<uint4*>(dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+      for (int x = 0; x < NB; ++x) {
+        if (at[x] == (size_t)-1) continue;
+        const uint32_t u[2] = {w[x].x, w[x].y};
+        uint32_t o[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int sh = 16 * (q & 1);
+          const float lo = (float)(int8_t)(u[q >> 1] >> sh) * sc[x];
+          const float hi = (float)(int8_t)(u[q >> 1] >> (sh + 8)) * sc[x];
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o[q]) : "f"(hi), "f"(lo));
+        }
+        *reinterpret_cast<uint4*>(((s0 + x) / blocks >= heads ? a.v_cache : a.k_cache) + at[x]) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+      }
     }
   }
 }
@@ -498,7 +512,9 @@ cudaError_t launch_paged_read(const PagedReadArgs& a0, int max_count, int sms, c
     per *= 2;
   a.heads_per_cta = per;
   const dim3 grid(pages, a.p.batch, (a.p.nkv + per - 1) / per);
-  paged_read_kernel<<<grid, 256, 0, s>>>(a);
+  if (a.p.hd == 64) paged_read_kernel<64><<<grid, 256, 0, s>>>(a);
+  else if (a.p.hd == 128) paged_read_kernel<128><<<grid, 256, 0, s>>>(a);
+  else paged_read_kernel<256><<<grid, 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
