@@ -91,8 +91,55 @@ cudaError_t launch_paged_block(const PagedAttnArgs& a, int slots, int splits, cu
 cudaError_t launch_paged_step(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,
                               long long blocks, int max_rows, int sms, cudaStream_t s);
 
+// Launches a kernel that may start while the one before it ends: it waits for that one
+// (pdl_wait) before its first access to global memory and to tensor memory.  2 us a call at the
+// head of a kernel (1 token, 1K keys: 18.5 -> 16 us).  None of these kernels lets the one behind
+// it start before its own end: that one may be of another file and read before it waits.
+template <class... P, class... T>
+cudaError_t paged_launch(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s,
+                         T... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ------------------------------------------------------------------ device helpers
 #ifdef __CUDACC__
+// Loads of data that the kernel before may have written.  They stay behind pdl_wait, where a
+// load declared read-only (__ldg) could be moved before it, or find a line that this SM's L1
+// took in before.
+__device__ __forceinline__ int ld_global(const int* p) {
+  int x;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ float ld_global(const float* p) {
+  float x;
+  asm volatile("ld.global.b32 %0, [%1];" : "=f"(x) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint2 ld_global(const uint2* p) {
+  uint2 x;
+  asm volatile("ld.global.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ uint4 ld_global(const uint4* p) {
+  uint4 x;
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "l"(p));
+  return x;
+}
+__device__ __forceinline__ float4 ld_global(const float4* p) {
+  const uint4 x = ld_global(reinterpret_cast<const uint4*>(p));
+  return make_float4(__uint_as_float(x.x), __uint_as_float(x.y), __uint_as_float(x.z), __uint_as_float(x.w));
+}
 // The same by shared-window address (no generic pointer to convert in a loop).
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;

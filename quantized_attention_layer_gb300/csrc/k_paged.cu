@@ -24,7 +24,7 @@ namespace {
 constexpr int kAppendThreads = 256;  // most threads of an append CTA
 
 __device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 a = ld_global(reinterpret_cast<const float4*>(p));
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
 }
 __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
@@ -171,6 +171,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(const P
   const PagedView& p = a.p;
   const int ps = p.ps;
   const int item = blockIdx.x;
+  pdl_wait();
   // sequence b owns items cu[b] / ps + 2 b .. : n rows touch at most n / ps + 2 pages
   int b;
   if (a.single) {
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(const P
   const int j = (start >> p.ps_log2) + (a.single ? 0 : item - ((row0 >> p.ps_log2) + 2 * b));
   const int page0 = j << p.ps_log2;  // position of the page's slot 0
   if (page0 >= start + n) return;
-  const int page = __ldg(p.table + (size_t)b * p.max_pages + j);  // checked below: the rows load meanwhile
+  const int page = ld_global(p.table + (size_t)b * p.max_pages + j);  // checked below: the rows load meanwhile
   const int first = max(start - page0, 0), last = min(start + n - page0, ps);
   const int c = threadIdx.x % U, slot0 = threadIdx.x / U;
   const int rstep = blockDim.x / U;
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(const P
     const float4* tab = a.slot_turn + ((size_t)slot * U + c) * 2;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float4 t = __ldg(tab + i), o = s_base[i * U + c];
+      const float4 t = ld_global(tab + i), o = s_base[i * U + c];
       cs[2 * i] = o.x * t.x - o.y * t.y;
       sn[2 * i] = o.y * t.x + o.x * t.y;
       cs[2 * i + 1] = o.z * t.z - o.w * t.w;
@@ -400,8 +401,7 @@ __global__ void __launch_bounds__(kAppendThreads, 4) paged_append_kernel(const P
 
 template <int HD, bool BIG, class T>
 cudaError_t launch_append(const PagedAppendArgs& a, dim3 grid, int threads, cudaStream_t s) {
-  paged_append_kernel<HD, BIG, T><<<grid, threads, 0, s>>>(a);
-  return cudaGetLastError();
+  return paged_launch(paged_append_kernel<HD, BIG, T>, grid, threads, 0, s, a);
 }
 template <class T>
 cudaError_t launch_append_t(const PagedAppendArgs& a, dim3 grid, int threads, bool big,
@@ -424,6 +424,7 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const PagedReadArgs a) 
   constexpr int U = HD / 8, RP = 256 / U, NB = 4;
   const PagedView& p = a.p;
   const int b = blockIdx.y;
+  pdl_wait();
   const int start = a.start[b], n = a.count[b];
   if (n <= 0) return;
   if (start < 0 || start > p.max_pages * p.ps - n || start > a.capacity - n) {
@@ -456,8 +457,8 @@ __global__ void __launch_bounds__(256) paged_read_kernel(const PagedReadArgs a) 
         at[x] = (size_t)-1;
         if (on) {
           const size_t pg = (size_t)page * p.nkv + kv;
-          sc[x] = __ldg((t ? p.v_scales : p.k_scales) + pg);
-          w[x] = __ldg(reinterpret_cast<const uint2*>((t ? p.v_codes : p.k_codes) + (pg * p.ps + slot) * HD) + c);
+          sc[x] = ld_global((t ? p.v_scales : p.k_scales) + pg);
+          w[x] = ld_global(reinterpret_cast<const uint2*>((t ? p.v_codes : p.k_codes) + (pg * p.ps + slot) * HD) + c);
           at[x] = (((size_t)b * p.nkv + kv) * a.capacity + page0 + slot) * HD + 8 * c;
         }
       }
@@ -512,10 +513,8 @@ cudaError_t launch_paged_read(const PagedReadArgs& a0, int max_count, int sms, c
     per *= 2;
   a.heads_per_cta = per;
   const dim3 grid(pages, a.p.batch, (a.p.nkv + per - 1) / per);
-  if (a.p.hd == 64) paged_read_kernel<64><<<grid, 256, 0, s>>>(a);
-  else if (a.p.hd == 128) paged_read_kernel<128><<<grid, 256, 0, s>>>(a);
-  else paged_read_kernel<256><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  auto kern = a.p.hd == 64 ? paged_read_kernel<64> : a.p.hd == 128 ? paged_read_kernel<128> : paged_read_kernel<256>;
+  return paged_launch(kern, grid, 256, 0, s, a);
 }
 
 }  // namespace hfa

@@ -240,6 +240,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
   const PagedView& p = a.p;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int G = p.nh / p.nkv;
+  pdl_wait();
   if (warp == 0) {
     BlockItem it;
     const bool on = block_item<HD>(a, splits, blockIdx.x, &it);
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
           const int R = it.r0 + j * 128 + r, tok = divg(R);
           w[i] = make_uint4(0u, 0u, 0u, 0u);
           if (j * 128 + r < it.rows)
-            w[i] = __ldg(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
+            w[i] = ld_global(reinterpret_cast<const uint4*>((const __nv_bfloat16*)a.q +
                                                         (size_t)(it.row0 + tok) * a.q_stride +
                                                         (size_t)(it.kvh * G + R - tok * G) * HD + 8 * c));
         }
@@ -557,7 +558,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     };
     const int* table = p.table + (size_t)it.b * p.max_pages;
     auto fetch_page = [&](int i) {
-      return wanted(i) ? __ldg(table + (((it.t0 + i) * KT + 16 * lane) >> p.ps_log2)) : 0;
+      return wanted(i) ? ld_global(table + (((it.t0 + i) * KT + 16 * lane) >> p.ps_log2)) : 0;
     };
     auto group_row = [&](int i, int pg) {
       if (!wanted(i)) return -1;
@@ -573,7 +574,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
         const int row = unit_row(x);
         const int base = __shfl_sync(0xffffffffu, grow0, row >> 4);
         if ((x + 1) * Cfg::NCW <= Cfg::NU || row < KT)
-          w[x] = __ldg(reinterpret_cast<const uint4*>(at + (size_t)(base + (row & 15)) * HD));
+          w[x] = ld_global(reinterpret_cast<const uint4*>(at + (size_t)(base + (row & 15)) * HD));
       }
     };
     auto store = [&](uint8_t* tile, const uint4 (&w)[PER]) {
@@ -593,8 +594,8 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     auto scales = [&](int gr, float& k, float& v) {
       k = v = 0.f;
       if (gr >= 0) {
-        k = __ldg(p.k_scales + (gr >> p.ps_log2));
-        v = __ldg(p.v_scales + (gr >> p.ps_log2));
+        k = ld_global(p.k_scales + (gr >> p.ps_log2));
+        v = ld_global(p.v_scales + (gr >> p.ps_log2));
       }
     };
     // in flight: the codes and scales of tile i + 1, the table entries of tile i + 2
@@ -804,19 +805,9 @@ cudaError_t launch_block_hd(const PagedAttnArgs& a, int slots, int splits, cudaS
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
   if (e != cudaSuccess) return e;
   const int units = slots * a.p.nkv;
-  kern<<<units * splits, Cfg::THREADS, Cfg::SMEM, s>>>(a, splits);
-  e = cudaGetLastError();
+  e = paged_launch(kern, dim3((unsigned)(units * splits)), Cfg::THREADS, Cfg::SMEM, s, a, splits);
   if (e != cudaSuccess || splits == 1) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * (Cfg::ROWS / 8)));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_block_merge_kernel<HD>, a, splits);
+  return paged_launch(paged_block_merge_kernel<HD>, dim3((unsigned)(units * (Cfg::ROWS / 8))), 256, 0, s, a, splits);
 }
 
 }  // namespace

@@ -72,9 +72,9 @@ struct SeqPlan {
 };
 __device__ __forceinline__ SeqPlan plan_seq(const PagedAttnArgs& a, int b, int G) {
   SeqPlan s;
-  s.row0 = __ldg(a.cu + b);
-  s.n = __ldg(a.cu + b + 1) - s.row0;
-  s.len = __ldg(a.len + b);
+  s.row0 = ld_global(a.cu + b);
+  s.n = ld_global(a.cu + b + 1) - s.row0;
+  s.len = ld_global(a.len + b);
   s.lo = 0;
   s.blocks = 0;
   if (s.n <= 0 || s.n * G > kPagedStepRows || s.row0 < 0 || s.row0 > a.total - s.n) return s;
@@ -88,6 +88,14 @@ __device__ __forceinline__ SeqPlan plan_seq(const PagedAttnArgs& a, int b, int G
   s.blocks = ((s.len + 15) >> 4) - s.lo;
   if (s.blocks < 1) s.blocks = 1;
   return s;
+}
+
+// Adds 1 by one thread between two barriers: covers the accesses of the whole CTA before the
+// first and after the second, cheaper than a fence by every thread.
+__device__ __forceinline__ int ticket_add(int* at) {
+  int before;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(at) : "memory");
+  return before;
 }
 
 template <int HD>
@@ -117,6 +125,11 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
     for (int i = 0; i < ns; ++i) mbar_init(&bars[i], 1);
     fence_barrier_init();
   }
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tmk);
+    prefetch_tmap(&tmv);
+  }
+  pdl_wait();  // the launch overlaps the end of the kernel before it, nothing else does
   // ------------------------------------------------------------------ prefix over the batch
   {
     const int per = (p.batch + NC * 32 - 1) / (NC * 32);
@@ -191,7 +204,7 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
       const int key0 = (s.lo + (int)(u - (uint32_t)kvh_next * (uint32_t)s.blocks)) << 4;
       if (key0 < s.len) {
         key_next = key0;
-        pg_next = __ldg(p.table + (size_t)b * p.max_pages + (key0 >> p.ps_log2));
+        pg_next = ld_global(p.table + (size_t)b * p.max_pages + (key0 >> p.ps_log2));
       }
     }
   };
@@ -202,8 +215,8 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
     if (key_next >= 0) {
       if ((unsigned)pg_next < (unsigned)p.num_pages) {
         const size_t u = (size_t)pg_next * p.nkv + kvh_next;
-        ks_next = __ldg(p.k_scales + u);
-        vs_next = __ldg(p.v_scales + u);
+        ks_next = ld_global(p.k_scales + u);
+        vs_next = ld_global(p.v_scales + u);
         row_next = (int)u * p.ps + (key_next & (p.ps - 1));
       } else {
         atomicOr(p.err, kErrBadPosition);
@@ -239,21 +252,6 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
     }
     ++issued;
   };
-  fetch_pages(0);
-  fetch_scales();
-  for (int i = 0; i < ns; ++i) advance(ring0 + i * Cfg::SLOT, bar0 + 8 * i);
-  // shared offsets of this lane's ldmatrix rows: rows 0..15 of a tile, 16-byte chunk c + (lane / 16)
-  uint32_t off[KS / 2];
-#pragma unroll
-  for (int c = 0; c < KS; c += 2)
-    off[c / 2] = tile_addr<Cfg>(0, ((lane >> 3) & 1) * 8 + (lane & 7), 16 * (c + (lane >> 4)));
-
-  // ------------------------------------------------------------------ pieces of units
-  bool dead = false;  // a wait gave up: no more reads, the barriers still match
-  int pos = warp, use = 0;  // the next block: its place in the CTA's range, its lane in the batch
-  uint32_t slot = ring0, bar = bar0, phase = 0;
-  const uint32_t ring_end = ring0 + ns * Cfg::SLOT;
-  long long at = t0;   // first block of the piece
   // one row of a unit's queries (row = token * G + head) is one warp's to fetch, a piece ahead,
   // and to turn into fragments; a lane holds quads lane, lane + 32, ... of it, zeros past its end
   static_assert(NC == kPagedStepRows, "a warp per row");
@@ -271,16 +269,31 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
       raw[j][0] = raw[j][1] = make_uint2(0u, 0u);
       if (warp < s.n * G && d < HD) {
         if (a.f32) {
-          const uint4 v = __ldg(reinterpret_cast<const uint4*>((const float*)a.q + qo + d));
+          const uint4 v = ld_global(reinterpret_cast<const uint4*>((const float*)a.q + qo + d));
           raw[j][0] = make_uint2(v.x, v.y);
           raw[j][1] = make_uint2(v.z, v.w);
         } else {
-          raw[j][0] = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)a.q + qo + d));
+          raw[j][0] = ld_global(reinterpret_cast<const uint2*>((const __nv_bfloat16*)a.q + qo + d));
         }
       }
     }
   };
+  fetch_pages(0);
   if (t0 < t1) fetch_row(t0);
+  fetch_scales();
+  for (int i = 0; i < ns; ++i) advance(ring0 + i * Cfg::SLOT, bar0 + 8 * i);
+  // shared offsets of this lane's ldmatrix rows: rows 0..15 of a tile, 16-byte chunk c + (lane / 16)
+  uint32_t off[KS / 2];
+#pragma unroll
+  for (int c = 0; c < KS; c += 2)
+    off[c / 2] = tile_addr<Cfg>(0, ((lane >> 3) & 1) * 8 + (lane & 7), 16 * (c + (lane >> 4)));
+
+  // ------------------------------------------------------------------ pieces of units
+  bool dead = false;  // a wait gave up: no more reads, the barriers still match
+  int pos = warp, use = 0;  // the next block: its place in the CTA's range, its lane in the batch
+  uint32_t slot = ring0, bar = bar0, phase = 0;
+  const uint32_t ring_end = ring0 + ns * Cfg::SLOT;
+  long long at = t0;   // first block of the piece
   while (at < t1) {
     const int b = seq_of(at, 0);
     const SeqPlan sq = plan_seq(a, b, G);
@@ -506,12 +519,8 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
       const int first = (int)(((v0 + 1) * A - 1) / V), last = (int)(((v0 + sq.blocks) * A - 1) / V);
       const int parts = last - first + 1;
       const int unit = b * p.nkv + kvh;
-      __threadfence();
       __syncthreads();
-      if (threadIdx.x == 0) {
-        s_misc[0] = atomicAdd(a.tickets + unit, 1) == parts - 1;
-        __threadfence();
-      }
+      if (threadIdx.x == 0) s_misc[0] = ticket_add(a.tickets + unit) == parts - 1;
       __syncthreads();
       if (s_misc[0]) {
         if (threadIdx.x == 0) a.tickets[unit] = 0;
@@ -620,8 +629,7 @@ cudaError_t launch_step_hd(const PagedAttnArgs& a, const CUtensorMap& tk, const 
   if (grid > (long long)sms * Cfg::CPS) grid = (long long)sms * Cfg::CPS;
   if (grid > kPagedMaxParts) grid = kPagedMaxParts;
   if (grid < 1) grid = 1;
-  paged_step_kernel<HD><<<(unsigned)grid, Cfg::NC * 32, smem, s>>>(tk, tv, a, ns, max_rows);
-  return cudaGetLastError();
+  return paged_launch(paged_step_kernel<HD>, dim3((unsigned)grid), Cfg::NC * 32, smem, s, tk, tv, a, ns, max_rows);
 }
 
 }  // namespace
