@@ -6,7 +6,8 @@
 //
 // Memory-bound: every code is read once.  The keys of all (sequence, KV head) units are one
 // list of 16-key blocks (a block never straddles a page, so it has one K and one V scale),
-// dealt out in equal contiguous ranges over the CTAs whatever the lengths of the sequences.
+// dealt out in equal contiguous ranges over the CTAs whatever the lengths of the sequences
+// (a unit counts for a few blocks more than it has).
 // Inside a CTA the warps take blocks in turn; each warp streams its own blocks through its
 // own ring of shared-memory slots by TMA (swizzled boxes of 16 rows), so no warp waits for
 // another until the range leaves a unit.  Table entries and scales are fetched 32 blocks at
@@ -52,8 +53,10 @@ struct StepCfg {
 
 constexpr float kNoMax = -1e30f;  // "no score yet"; finite, so differences are never NaN
 // What a unit costs beside its blocks (queries, barriers, merge), in blocks: the ranges are
-// dealt out over blocks + this when there are about as many units as CTAs or more.  Fitted to
-// the cycles of CTAs with 3 and with 9 pieces of 64 ragged sequences: 11200 a piece, 303 a block.
+// dealt out over blocks + this.  Fitted to the cycles of CTAs with 3 and with 9 pieces of 64
+// ragged sequences: 11200 a piece, 303 a block.  So a short range also never holds the end of
+// one unit and the beginning of the next (1 token, 1K keys 15.2 -> 10 us, 8 such sequences 20
+// -> 14.7; 24 and 52 differ by 0 to 2 %).
 constexpr int kUnitCost = 36;
 constexpr float kLazy = 8.f;      // how far (log2) a score may exceed the running maximum
 
@@ -156,12 +159,12 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
     __syncthreads();
   }
   const long long W = (long long)pre[p.batch] * p.nkv;  // all blocks
-  // CTAs at work: every warp has a block before another CTA joins
-  long long A = (W + NC - 1) / NC;
+  constexpr int cost = kUnitCost;
+  const long long V = W + (long long)cost * p.batch * p.nkv;  // blocks and the units' costs
+  // CTAs at work: two blocks a warp before another CTA joins (one: 4K keys 13.0 -> 14.1 us)
+  long long A = (V + 2 * NC - 1) / (2 * NC);
   if (A > gridDim.x) A = gridDim.x;
   if (blockIdx.x >= A) return;
-  const int cost = 2 * p.batch * p.nkv >= A ? kUnitCost : 0;
-  const long long V = W + (long long)cost * p.batch * p.nkv;  // blocks and the units' costs
   // the last sequence b with (pre[b] + cost b) nkv <= x
   auto seq_of = [&](long long x, int cost) {
     int lo = 0, hi = p.batch;
@@ -625,7 +628,7 @@ cudaError_t launch_step_hd(const PagedAttnArgs& a, const CUtensorMap& tk, const 
   const size_t smem = fixed + (size_t)ns * Cfg::NC * Cfg::SLOT;
   cudaError_t e = cudaFuncSetAttribute(paged_step_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  long long grid = (blocks + Cfg::NC - 1) / Cfg::NC;
+  long long grid = (blocks + (long long)kUnitCost * a.p.batch * a.p.nkv + 2 * Cfg::NC - 1) / (2 * Cfg::NC);
   if (grid > (long long)sms * Cfg::CPS) grid = (long long)sms * Cfg::CPS;
   if (grid > kPagedMaxParts) grid = kPagedMaxParts;
   if (grid < 1) grid = 1;
