@@ -64,7 +64,8 @@ struct PagedAttnArgs {
   int window, bidir;
   float qscale;         // scale * log2 e, or scale / softcap
   float cap_log2;       // softcap * log2 e, 0 = none
-  int* tickets;         // [batch * nkv], zero between calls: parts of a unit that are done
+  int* tickets;         // [kPagedMaxParts], zero between calls: parts of a unit that are done, at the
+                        // number of the unit's first CTA (a CTA is the first of one shared unit at most)
   float* records;       // [2 * kPagedMaxParts][kPagedStepRows][kPagedRecord(hd)]
   float* block_records;  // [CTAs][rows of a CTA][kPagedRecord(hd)], with splits > 1
 };

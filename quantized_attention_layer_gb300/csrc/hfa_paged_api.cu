@@ -167,15 +167,16 @@ hfa_status check_written(hfa_paged* p, int batch, const int32_t* cu, const int32
   return st;
 }
 
-// workspace: [tickets, 256-byte aligned][records of the step kernel][records of the block
-// kernel, when its (row tile, KV head) slots are few enough to be shared by several CTAs]
+// workspace: [tickets][records of the step kernel][records of the block kernel, when its (row
+// tile, KV head) slots are few enough to be shared by several CTAs].  The tickets, which have to
+// be zero when a call begins, lie at the same place for every batch and handle.
 long long block_slots(const hfa_paged_desc& d, int batch, int total) {
   return (long long)total * (d.num_heads / d.num_kv_heads) / hfa::paged_block_rows(d.head_dim) + batch;
 }
 long long block_units(const hfa_paged_desc& d, int batch, int total) {
   return block_slots(d, batch, total) * d.num_kv_heads;
 }
-size_t ticket_bytes(int batch, int nkv) { return ((size_t)batch * nkv * sizeof(int) + 255) / 256 * 256; }
+constexpr size_t kTicketBytes = (hfa::kPagedMaxParts * sizeof(int) + 255) / 256 * 256;
 size_t record_bytes(int hd) {
   return (size_t)2 * hfa::kPagedMaxParts * hfa::kPagedStepRows * hfa::kPagedRecord(hd) * sizeof(float);
 }
@@ -349,14 +350,13 @@ extern "C" hfa_status hfa_paged_append(hfa_paged* p, void* stream, int batch, co
 
 extern "C" size_t hfa_paged_workspace_bytes(const hfa_paged* p, int batch, int total_rows) {
   if (!p || batch < 1 || batch > 4096 || total_rows < 0) return 0;
-  const size_t tickets = ticket_bytes(batch, p->d.num_kv_heads);
   const int G = p->d.num_heads / p->d.num_kv_heads;
   size_t blocks = 0;
   if ((long long)total_rows * G > hfa::kPagedStepRows &&
       block_units(p->d, batch, total_rows) * 2 <= hfa::kPagedMaxParts)
     blocks = (size_t)hfa::kPagedMaxParts * hfa::paged_block_rows(p->d.head_dim) *
              hfa::kPagedRecord(p->d.head_dim) * sizeof(float);
-  return tickets + record_bytes(p->d.head_dim) + blocks;
+  return kTicketBytes + record_bytes(p->d.head_dim) + blocks;
 }
 
 extern "C" hfa_status hfa_paged_attention(hfa_paged* p, void* stream, int batch,
@@ -407,7 +407,7 @@ extern "C" hfa_status hfa_paged_attention(hfa_paged* p, void* stream, int batch,
   a.qscale = d.softcap > 0.f ? d.attn_scale / d.softcap : d.attn_scale * log2e;
   a.cap_log2 = d.softcap * log2e;
   a.tickets = (int*)ws;
-  a.records = (float*)((char*)ws + ticket_bytes(batch, d.num_kv_heads));
+  a.records = (float*)((char*)ws + kTicketBytes);
   // the sequences of few rows, and the others
   const int G = d.num_heads / d.num_kv_heads;
   long long blocks = 0;

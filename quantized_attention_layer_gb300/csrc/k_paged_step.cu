@@ -521,12 +521,11 @@ __global__ void __launch_bounds__(StepCfg<HD>::NC * 32, StepCfg<HD>::CPS)
       const long long v0 = u0 + (long long)cost * ((long long)b * p.nkv + kvh + 1);  // first block's place
       const int first = (int)(((v0 + 1) * A - 1) / V), last = (int)(((v0 + sq.blocks) * A - 1) / V);
       const int parts = last - first + 1;
-      const int unit = b * p.nkv + kvh;
       __syncthreads();
-      if (threadIdx.x == 0) s_misc[0] = ticket_add(a.tickets + unit) == parts - 1;
+      if (threadIdx.x == 0) s_misc[0] = ticket_add(a.tickets + first) == parts - 1;
       __syncthreads();
       if (s_misc[0]) {
-        if (threadIdx.x == 0) a.tickets[unit] = 0;
+        if (threadIdx.x == 0) a.tickets[first] = 0;
         // record i of the unit: CTA first + i, its tail piece (slot 1) for i = 0
         auto rec = [&](int i, int r) {
           return a.records + (((size_t)(first + i) * 2 + (i == 0)) * kPagedStepRows + r) * RS;

@@ -649,3 +649,130 @@ def test_refusals_with_a_handle():
     assert status(lambda: p2.hfa_paged_read(ref.dev(z), z, ref.dev(z), z, pool.pages, cache, cache)) == hfa.HFA_EINVAL
     torch.cuda.synchronize()
     p.hfa_paged_check_status()
+
+
+def test_one_workspace_for_calls_of_every_size():
+    """A workspace as large as the largest call needs, used by calls of other batch sizes, row
+    counts and handles in turn, eagerly and by two captured graphs: each finds it as a fresh one."""
+    rng = np.random.default_rng(61)
+    sides = []
+    for nh, nkv, hd, ps, ns, lens in ((8, 2, 128, 16, [1], [3000]), (4, 4, 64, 32, [1] * 90, None),
+                                      (8, 2, 128, 16, [20, 1], [900, 1200]), (2, 1, 256, 64, [2, 40, 1], [500, 700, 1])):
+        lens = np.asarray(lens if lens is not None else rng.integers(1, 400, len(ns)), dtype=np.int32)
+        mx = -(-int(lens.max()) // ps)
+        table, num = ref.make_table(rng, [-(-int(n) // ps) for n in lens], mx)
+        arrays = ref.make_pool(rng, num, nkv, ps, hd)
+        cu = ref.ragged(ns)
+        T = int(cu[-1])
+        s = dict(p=make(nh, nkv, hd, ps, num, mx), pool=Pool(arrays, table), cu=cu, cud=ref.dev(cu), lens=lens,
+                 ld=ref.dev(lens), q=draw_rows(rng, T, nh, hd, torch.bfloat16).cuda())
+        s["o"] = torch.empty_like(s["q"])
+        s["bytes"] = s["p"].hfa_paged_workspace_bytes(len(ns), T)
+        s["want"], bound = ref.attend(s["q"].double().cpu().numpy(), cu, lens, arrays, table, ps, hd ** -0.5)
+        s["bound"] = bound + ref.BF16 * np.abs(s["want"]) + ref.BF16 * bound / 2.0 ** -19
+        sides.append(s)
+    ws = torch.zeros(max(s["bytes"] for s in sides), dtype=torch.uint8, device="cuda")
+
+    def call(s):
+        s["p"].hfa_paged_attention(s["cud"], s["cu"], s["ld"], s["lens"], s["q"], s["pool"].pages, ws, s["o"])
+
+    def check(s):
+        s["p"].hfa_paged_check_status()
+        assert np.all(np.abs(s["o"].double().cpu().numpy() - s["want"]) <= s["bound"])
+        s["o"].fill_(float("nan"))
+
+    for i in (0, 1, 2, 3, 1, 0, 2, 1, 3, 0):
+        call(sides[i])
+        check(sides[i])
+    stream = torch.cuda.Stream()
+    graphs = []
+    torch.cuda.synchronize()
+    for s in sides:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=stream):
+            call(s)
+    for i in (1, 0, 3, 1, 2, 0, 1):
+        with torch.cuda.stream(stream):
+            graphs[i].replay()
+        stream.synchronize()
+        check(sides[i])
+
+
+def test_launches_that_overlap_wait_for_their_inputs():
+    """Calls in a row on one stream, each reading what the kernel before wrote, that one being
+    slow: another library's copy, an append, an attention, a read; eagerly, captured, and
+    captured with the queries written on a second stream."""
+    rng = np.random.default_rng(71)
+    nh, nkv, hd, ps, mx = 8, 2, 128, 16, 8
+    table, num = ref.make_table(rng, [mx], mx)
+    p = make(nh, nkv, hd, ps, num, mx)
+    x = draw_rows(rng, 100, nh + 2 * nkv, hd, torch.bfloat16).cuda()
+    cu, start, lens = ref.ragged([100]), np.zeros(1, dtype=np.int32), np.array([100], dtype=np.int32)
+    one, l1 = ref.ragged([1]), np.array([100], dtype=np.int32)
+    cud, sd, ld, oned, l1d = ref.dev(cu, start, lens, one, l1)
+    arrays = ref.make_pool(rng, num, nkv, ps, hd)
+    ws = torch.zeros(p.hfa_paged_workspace_bytes(1, 100), dtype=torch.uint8, device="cuda")
+    side, main = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def fresh():
+        kc = torch.zeros((1, nkv, 128, hd), dtype=torch.bfloat16, device="cuda")
+        o = torch.empty((100, nh, hd), dtype=torch.bfloat16, device="cuda")
+        return dict(pool=Pool(arrays, table), x=torch.zeros_like(x), q=torch.zeros_like(o), o=o, o1=torch.zeros_like(o[:1]),
+                    kc=kc, vc=torch.zeros_like(kc))
+
+    def chain(s, forked, wait):
+        def write():
+            if wait:
+                torch.cuda._sleep(2_000_000)
+            s["x"].copy_(x)
+
+        if forked:
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                write()
+            main.wait_stream(side)
+        else:
+            write()
+        y = s["x"]
+        p.hfa_paged_append(cud, cu, sd, start, y[:, :nh], y[:, nh:nh + nkv], y[:, nh + nkv:], s["pool"].pages, s["q"])
+        p.hfa_paged_attention(cud, cu, ld, lens, s["q"], s["pool"].pages, ws, s["o"])
+        p.hfa_paged_attention(oned, one, l1d, l1, s["o"][99:], s["pool"].pages, ws, s["o1"])
+        p.hfa_paged_read(sd, start, ld, lens, s["pool"].pages, s["kc"], s["vc"])
+
+    def result(s):
+        return [s[n].clone() for n in ("q", "o", "o1", "kc", "vc")] + [s["pool"].k.clone(), s["pool"].vs.clone()]
+
+    # every kernel alone
+    s = fresh()
+    s["x"].copy_(x)
+    torch.cuda.synchronize()
+    p.hfa_paged_append(cud, cu, sd, start, x[:, :nh], x[:, nh:nh + nkv], x[:, nh + nkv:], s["pool"].pages, s["q"])
+    torch.cuda.synchronize()
+    p.hfa_paged_attention(cud, cu, ld, lens, s["q"], s["pool"].pages, ws, s["o"])
+    torch.cuda.synchronize()
+    p.hfa_paged_attention(oned, one, l1d, l1, s["o"][99:], s["pool"].pages, ws, s["o1"])
+    torch.cuda.synchronize()
+    p.hfa_paged_read(sd, start, ld, lens, s["pool"].pages, s["kc"], s["vc"])
+    want = result(s)
+    assert float(want[2].abs().max()) > 0
+    for forked in (False, True):
+        s = fresh()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(main):
+            chain(s, forked, True)
+        main.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(result(s), want))
+        s = fresh()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            chain(s, forked, True)
+        for _ in range(3):
+            for t in ("x", "q", "o", "o1", "kc", "vc"):
+                s[t].zero_()
+            torch.cuda.synchronize()
+            with torch.cuda.stream(main):
+                graph.replay()
+            main.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(result(s), want))
+    p.hfa_paged_check_status()
