@@ -555,6 +555,9 @@ class Pages:
             raise HfaError(HFA_EINVAL, "k_codes and v_codes are [num_pages, nkv, page_size, hd]")
         if k_scales.shape != k_codes.shape[:2] or v_scales.shape != k_codes.shape[:2]:
             raise HfaError(HFA_EINVAL, "the scales are [num_pages, nkv]")
+        self.device = k_codes.get_device()
+        if self.device < 0 or any(t.get_device() != self.device for t in (k_scales, v_codes, v_scales, table)):
+            raise HfaError(HFA_EINVAL, "the pool and the table must be on one CUDA device")
         if table.dim() != 2:
             raise HfaError(HFA_EINVAL, "the table is [batch, max_pages]")
         if table_host is not None:
@@ -579,8 +582,8 @@ class Paged:
         self._h = ctypes.c_void_p()
         for w in (w_q, w_k):
             if w is not None and (w.dtype != torch.float32 or w.numel() != desc.head_dim or
-                                  not w.is_contiguous()):
-                raise HfaError(HFA_EINVAL, "w_q and w_k are f32 [head_dim]")
+                                  not w.is_contiguous() or not w.is_cuda):
+                raise HfaError(HFA_EINVAL, "w_q and w_k are f32 [head_dim] on the device")
         if rope_factors is not None:
             rope_factors = np.ascontiguousarray(rope_factors, dtype=np.float32)
             if rope_factors.size != desc.head_dim // 2:
@@ -594,6 +597,7 @@ class Paged:
             raise HfaError(st, lib().hfa_paged_last_error(None).decode())
         self._shape = (desc.num_pages, desc.num_kv_heads, desc.page_size, desc.head_dim, desc.max_pages)
         self._nh, self._nkv, self._hd = desc.num_heads, desc.num_kv_heads, desc.head_dim
+        self._dev = torch.cuda.current_device()
 
     def _check(self, st: int):
         if st != HFA_OK:
@@ -602,6 +606,8 @@ class Paged:
     def _pages(self, pages: Pages, batch: int) -> None:
         if pages.shape != self._shape:
             raise HfaError(HFA_EINVAL, f"a pool and table {pages.shape}, the cache is {self._shape}")
+        if pages.device != self._dev:
+            raise HfaError(HFA_EINVAL, f"a pool on device {pages.device}, the cache is on {self._dev}")
         if pages.batch < batch or batch < 1:
             raise HfaError(HFA_EINVAL, f"{batch} sequences, the table has {pages.batch}")
 
@@ -611,6 +617,8 @@ class Paged:
         if x.shape != (total, heads, hd) or x.dtype is not dtype:
             raise HfaError(HFA_EINVAL, f"rows {tuple(x.shape)} {x.dtype}, expected "
                                        f"{(total, heads, hd)} {dtype}")
+        if x.get_device() != self._dev:
+            raise HfaError(HFA_EINVAL, f"rows on {x.device}, the cache is on device {self._dev}")
         s0, s1, s2 = x.stride()
         if total and (s2 != 1 or (s1 != hd and heads > 1)):
             raise HfaError(HFA_EINVAL, "the heads of a row must be dense")
@@ -625,8 +633,8 @@ class Paged:
     def hfa_paged_append(self, cu_dev: torch.Tensor, cu_host, start_dev: torch.Tensor, start_host,
                          q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, pages: Pages,
                          q_out: Optional[torch.Tensor] = None, stream=None) -> None:
-        cu, cup = _ints(cu_host, cu_dev)
-        start, startp = _ints(start_host, start_dev)
+        cu, cup = _ints(cu_host, cu_dev, self._dev)
+        start, startp = _ints(start_host, start_dev, self._dev)
         batch = start.size
         self._pages(pages, batch)
         total = _total(cu, batch)
@@ -651,13 +659,15 @@ class Paged:
     def hfa_paged_attention(self, cu_dev: torch.Tensor, cu_host, len_dev: torch.Tensor, len_host,
                             q: torch.Tensor, pages: Pages, workspace: torch.Tensor, o: torch.Tensor,
                             stream=None) -> torch.Tensor:
-        cu, cup = _ints(cu_host, cu_dev)
-        lens, lenp = _ints(len_host, len_dev)
+        cu, cup = _ints(cu_host, cu_dev, self._dev)
+        lens, lenp = _ints(len_host, len_dev, self._dev)
         batch = lens.size
         self._pages(pages, batch)
         total = _total(cu, batch)
         qp, qs = self._rows(q, self._nh, total, q.dtype)
         op = self._dense(o, total, q.dtype)
+        if workspace.get_device() != self._dev or not workspace.is_contiguous():
+            raise HfaError(HFA_EINVAL, f"the workspace must be contiguous on device {self._dev}")
         st = lib().hfa_paged_attention(self._h, _stream_handle(stream), batch, cu_dev.data_ptr(), cup,
                                        len_dev.data_ptr(), lenp, qp, qs, _row_type(q.dtype),
                                        pages.ref, workspace.data_ptr(), workspace.nbytes, op)
@@ -667,8 +677,8 @@ class Paged:
 
     def hfa_paged_read(self, start_dev: torch.Tensor, start_host, count_dev: torch.Tensor, count_host,
                        pages: Pages, k_cache: torch.Tensor, v_cache: torch.Tensor, stream=None) -> None:
-        start, startp = _ints(start_host, start_dev)
-        count, countp = _ints(count_host, count_dev)
+        start, startp = _ints(start_host, start_dev, self._dev)
+        count, countp = _ints(count_host, count_dev, self._dev)
         batch = start.size
         self._pages(pages, batch)
         if count.size != batch:
@@ -678,8 +688,8 @@ class Paged:
                 v_cache.shape != shape:
             raise HfaError(HFA_EINVAL, f"the caches are [{batch}, {self._nkv}, capacity, {self._hd}]")
         for c in (k_cache, v_cache):
-            if c.dtype is not torch.bfloat16 or not c.is_contiguous():
-                raise HfaError(HFA_EINVAL, "the caches must be contiguous bf16")
+            if c.dtype is not torch.bfloat16 or not c.is_contiguous() or c.get_device() != self._dev:
+                raise HfaError(HFA_EINVAL, f"the caches must be contiguous bf16 on device {self._dev}")
         st = lib().hfa_paged_read(self._h, _stream_handle(stream), batch, start_dev.data_ptr(), startp,
                                   count_dev.data_ptr(), countp, pages.ref, shape[2],
                                   k_cache.data_ptr(), v_cache.data_ptr())
@@ -701,11 +711,13 @@ class Paged:
             pass
 
 
-def _ints(host, dev: torch.Tensor) -> tuple:
-    """(host int32 array, its address) of one per-sequence argument and its device copy."""
+def _ints(host, dev: torch.Tensor, device: int) -> tuple:
+    """(host int32 array, its address) of one per-sequence argument; checks its device copy."""
     a = np.ascontiguousarray(host, dtype=np.int32)
-    if dev.dtype is not torch.int32 or dev.numel() < a.size or not dev.is_contiguous():
-        raise HfaError(HFA_EINVAL, f"the device copy of {a.size} integers: {dev.numel()} of {dev.dtype}")
+    if dev.dtype is not torch.int32 or dev.numel() < a.size or not dev.is_contiguous() or \
+            dev.get_device() != device:
+        raise HfaError(HFA_EINVAL, f"the device copy of {a.size} integers: {dev.numel()} of {dev.dtype} "
+                                   f"on {dev.device}")
     if a.size == 0 or not a.flags.writeable:  # from_buffer takes neither
         return a, a.ctypes.data
     return a, ctypes.addressof(ctypes.c_char.from_buffer(a))

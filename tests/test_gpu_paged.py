@@ -776,3 +776,36 @@ def test_launches_that_overlap_wait_for_their_inputs():
             main.synchronize()
             assert all(torch.equal(a, b) for a, b in zip(result(s), want))
     p.hfa_paged_check_status()
+
+
+def test_refuses_tensors_off_the_device():
+    table = np.array([[0, 1]], dtype=np.int32)
+    arrays = ref.make_pool(np.random.default_rng(0), 2, 1, 16, 64)
+    pool = Pool(arrays, table)
+    with pytest.raises(hfa.HfaError) as e:
+        hfa.Pages(pool.k.cpu(), pool.ks, pool.v, pool.vs, pool.table, table)
+    assert e.value.status == hfa.HFA_EINVAL
+    with pytest.raises(hfa.HfaError):
+        hfa.Pages(pool.k, pool.ks, pool.v, pool.vs, pool.table.cpu(), table)
+    with pytest.raises(hfa.HfaError):
+        make(1, 1, 64, 16, 2, 2, w_q=torch.ones(64))
+    p = make(1, 1, 64, 16, 2, 2)
+    cu, z, ln = ref.ragged([1]), np.zeros(1, dtype=np.int32), np.ones(1, dtype=np.int32)
+    cud, zd, ld = ref.dev(cu, z, ln)
+    x = torch.zeros((1, 1, 64), device="cuda")
+    cache = torch.zeros((1, 1, 16, 64), dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(p.hfa_paged_workspace_bytes(1, 1), dtype=torch.uint8, device="cuda")
+
+    def off(call, args):
+        """Every tensor argument in turn in host memory."""
+        call(*args)
+        for i, a in enumerate(args):
+            if isinstance(a, torch.Tensor):
+                with pytest.raises(hfa.HfaError) as e:
+                    call(*args[:i], a.cpu(), *args[i + 1:])
+                assert e.value.status == hfa.HFA_EINVAL
+
+    off(p.hfa_paged_append, [cud, cu, zd, z, x, x.clone(), x.clone(), pool.pages, x.clone()])
+    off(p.hfa_paged_attention, [cud, cu, ld, ln, x, pool.pages, ws, x.clone()])
+    off(p.hfa_paged_read, [zd, z, ld, ln, pool.pages, cache, cache.clone()])
+    p.hfa_paged_check_status()
