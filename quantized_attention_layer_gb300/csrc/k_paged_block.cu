@@ -549,30 +549,34 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       const int row = unit_row(x);
       place[x] = (chunk >> 2) * Cfg::KBOX + row * 128 + ((2 * (chunk & 3)) ^ (row & 7)) * 16;
     }
-    // lane g < NG looks after group g of a tile: the table entry (only fetched here: a warp
-    // stalls at the first use of what it loads), then the group's first row in the pools, -1
-    // when nothing of it is read (outside the visible keys), -2 for a refused page
-    auto wanted = [&](int i) {
-      const int k0 = (it.t0 + i) * KT + 16 * lane;
-      return i < nt && lane < NG && k0 < it.hi && k0 + 16 > it.lo;
+    // table entries and scales come TB tiles at a time, lane l's for group l % NG of the batch's
+    // tile l / NG: a warp that uses a load's result may wait for every later load too (they share
+    // scoreboards), so that happens twice a batch and not twice a tile
+    constexpr int TB = 32 / NG;
+    static_assert(TB >= 4, "entries, rows and scales are two tiles apart");
+    auto key_of = [&](int batch) { return (it.t0 + batch * TB + lane / NG) * KT + 16 * (lane % NG); };
+    auto wanted = [&](int batch) {
+      return batch * TB + lane / NG < nt && key_of(batch) < it.hi && key_of(batch) + 16 > it.lo;
     };
     const int* table = p.table + (size_t)it.b * p.max_pages;
-    auto fetch_page = [&](int i) {
-      return wanted(i) ? ld_global(table + (((it.t0 + i) * KT + 16 * lane) >> p.ps_log2)) : 0;
+    auto fetch_page = [&](int batch) {
+      return wanted(batch) ? ld_global(table + (key_of(batch) >> p.ps_log2)) : 0;
     };
-    auto group_row = [&](int i, int pg) {
-      if (!wanted(i)) return -1;
+    // the group's first row in the pools, -1 when nothing of it is read (outside the visible
+    // keys), -2 for a refused page
+    auto group_row = [&](int batch, int pg) {
+      if (!wanted(batch)) return -1;
       if ((unsigned)pg >= (unsigned)p.num_pages) return -2;
-      return (pg * p.nkv + it.kvh) * p.ps + (((it.t0 + i) * KT + 16 * lane) & (p.ps - 1));
+      return (pg * p.nkv + it.kvh) * p.ps + (key_of(batch) & (p.ps - 1));
     };
     // rows that nobody sees come from the pool's first row: finite codes of weight 0
-    auto load = [&](const int8_t* codes, int grow, uint4 (&w)[PER]) {
+    auto load = [&](const int8_t* codes, int rows, int i, uint4 (&w)[PER]) {  // tile i's
       const int8_t* at = codes + 16 * chunk;
-      const int grow0 = max(grow, 0);
+      const int rows0 = max(rows, 0), from = i % TB * NG;
 #pragma unroll
       for (int x = 0; x < PER; ++x) {
         const int row = unit_row(x);
-        const int base = __shfl_sync(0xffffffffu, grow0, row >> 4);
+        const int base = __shfl_sync(0xffffffffu, rows0, from + (row >> 4));
         if ((x + 1) * Cfg::NCW <= Cfg::NU || row < KT)
           w[x] = ld_global(reinterpret_cast<const uint4*>(at + (size_t)(base + (row & 15)) * HD));
       }
@@ -598,36 +602,44 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
         v = ld_global(p.v_scales + (gr >> p.ps_log2));
       }
     };
-    // in flight: the codes and scales of tile i + 1, the table entries of tile i + 2
+    // in flight: the codes of tile i + 1, the rows and scales of the next batch
     uint4 kw[PER], vw[PER];
-    float ks, vs, ks1, vs1;
-    int pg2 = fetch_page(1);
-    int grow = group_row(0, fetch_page(0)), grow1 = group_row(1, pg2);
-    load(p.k_codes, grow, kw);
-    load(p.v_codes, grow, vw);
+    float ks, vs, ks1 = 0.f, vs1 = 0.f;
+    int pg1 = 0;
+    int grow = group_row(0, fetch_page(0)), grow1 = -1;
+    load(p.k_codes, grow, 0, kw);
+    load(p.v_codes, grow, 0, vw);
     scales(grow, ks, vs);
     const bool lead = cw == 0;
     for (int i = 0; i < nt; ++i) {
-      const int st = i % NST, sc = i % NSC;
+      const int st = i % NST, sc = i % NSC, bt = i % TB;
       const uint32_t ph = ((i / NST) & 1) ^ 1;
-      pg2 = fetch_page(i + 2);
-      scales(grow1, ks1, vs1);
+      if (bt == 0) {
+        if (i > 0) grow = grow1, ks = ks1, vs = vs1;
+        pg1 = fetch_page(i / TB + 1);
+      } else if (bt == 2) {
+        grow1 = group_row(i / TB + 1, pg1);
+        scales(grow1, ks1, vs1);
+      }
+      const int grow_ahead = bt == TB - 1 ? grow1 : grow;  // of the batch of tile i + 1
       bool ok = i < NST || paged_wait(&k_free[st], ph, p.err, (const volatile int*)s_abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
         *s_abort = 1;
         break;
       }
+      const bool mine = lane / NG == bt;  // this lane's group is of tile i
       if (lead) {
-        const bool bad = grow == -2;
-        if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(p.err, kErrBadPosition);
-        if (lane < NG) {
+        const bool any_bad = __any_sync(0xffffffffu, mine && grow == -2);
+        if (mine) {
           const bool live = vs > 0.f;
-          s_sc[sc * NG + lane] = make_float4(grow >= 0 ? ks : -1.f, live ? log2f(vs) : kZeroLvs,
-                                             live ? 1.f / vs : 1.2676506e30f /* 2^100 */, 0.f);
+          s_sc[sc * NG + lane % NG] = make_float4(grow >= 0 ? ks : -1.f, live ? log2f(vs) : kZeroLvs,
+                                                  live ? 1.f / vs : 1.2676506e30f /* 2^100 */, 0.f);
         }
-        const bool any_bad = __any_sync(0xffffffffu, bad);
-        if (lane == 0) s_flag[sc] = any_bad;
+        if (lane == 0) {
+          s_flag[sc] = any_bad;
+          if (any_bad) atomicOr(p.err, kErrBadPosition);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sc_full[sc]);
       }
@@ -635,7 +647,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&k_full[st]);
-      load(p.k_codes, grow1, kw);
+      load(p.k_codes, grow_ahead, i + 1, kw);
       ok = i < NST || paged_wait(&v_free[st], ph, p.err, (const volatile int*)s_abort);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
@@ -643,7 +655,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
         break;
       }
       // pages with V scale 0 count as zeros, whatever their codes
-      const uint32_t zero = __ballot_sync(0xffffffffu, grow >= 0 && !(vs > 0.f));
+      const uint32_t zero = __ballot_sync(0xffffffffu, mine && grow >= 0 && !(vs > 0.f)) >> (bt * NG);
       if (zero) {
 #pragma unroll
         for (int x = 0; x < PER; ++x)
@@ -653,11 +665,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&v_full[st]);
-      load(p.v_codes, grow1, vw);
-      grow = grow1;
-      grow1 = group_row(i + 2, pg2);
-      ks = ks1;
-      vs = vs1;
+      load(p.v_codes, grow_ahead, i + 1, vw);
     }
   } else {
     // ================================================================== MMA issuer
