@@ -83,10 +83,11 @@ cudaError_t launch_paged_append(const PagedAppendArgs& a, bool f32, int items, i
 cudaError_t launch_paged_read(const PagedReadArgs& a, int max_count, int sms, cudaStream_t s);
 // The block kernel (k_paged_block.cu) serves the others, paged_block_rows(hd) rows x heads and
 // paged_block_keys(hd) keys at a time.  slots: total * G / rows + batch; splits (at most
-// kPagedMaxSplits): CTAs that share the keys of an item.
+// kPagedMaxSplits): CTAs that share the keys of an item; max_rows: most rows x heads of a KV head
+// of a sequence.
 int paged_block_rows(int hd);
 int paged_block_keys(int hd);
-cudaError_t launch_paged_block(const PagedAttnArgs& a, int slots, int splits, cudaStream_t s);
+cudaError_t launch_paged_block(const PagedAttnArgs& a, int slots, int splits, int max_rows, cudaStream_t s);
 // blocks: the 16-key blocks of the sequences it serves, times nkv; max_rows: their most rows x
 // heads of a KV head; tk, tv: byte views of the pools in boxes of 16 rows
 cudaError_t launch_paged_step(const PagedAttnArgs& a, const CUtensorMap& tk, const CUtensorMap& tv,

@@ -450,7 +450,7 @@ extern "C" hfa_status hfa_paged_attention(hfa_paged* p, void* stream, int batch,
     if (splits > most_tiles) splits = most_tiles;
     if (splits > hfa::kPagedMaxParts / units) splits = hfa::kPagedMaxParts / units;
     if (splits < 1) splits = 1;
-    e = hfa::launch_paged_block(a, (int)block_slots(d, batch, total), (int)splits, s);
+    e = hfa::launch_paged_block(a, (int)block_slots(d, batch, total), (int)splits, longest * G, s);
   }
   if (e != cudaSuccess) return fail(p, HFA_ECUDA, "attention launch: %s", cudaGetErrorString(e));
   return HFA_OK;

@@ -57,8 +57,6 @@ struct BlockCfg {
   static constexpr int NSC = 4;                   // scale slots (see sc_full)
   static constexpr int SMEM_OPS = QT * QTILE + 2 * NST * KTILE;
   static constexpr size_t SMEM = 1024 + SMEM_OPS + ROWS * 4 + NSC * (NG * 16 + 16) + 256;
-  // scores of one MMA: a whole tile of keys, or (hd 256) a step, in the other of two buffers
-  static constexpr int SN = QT == 2 ? KT : UK;
   static constexpr int O_COL = QT * 2 * UK;       // TMEM: two steps' S a row tile, then O
   static constexpr int CPR = HD / 16;             // 16-byte chunks of a row of codes
   static constexpr int RPU = 32 / CPR;            // rows of a converter's unit: 32 chunks
@@ -205,7 +203,11 @@ __device__ __forceinline__ bool block_item(const PagedAttnArgs& a, int splits, i
   return true;
 }
 
-template <int HD, bool CAP>
+// ONE: no CTA of the call has more than one row tile.  Its scores then come by steps, in the
+// other of two buffers, and run while a step is in its softmax; with two row tiles the other
+// tile's work does, and scores come by whole tiles (by steps they read Q twice).  16 rows of 4
+// sequences over 8K keys take 32.5 us by steps and 37.5 by tiles, an 8K prompt 458 and 412.
+template <int HD, bool CAP, bool ONE>
 __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     paged_block_kernel(const PagedAttnArgs a, int splits) {
   using Cfg = BlockCfg<HD>;
@@ -228,7 +230,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
   uint64_t* sc_full = v_free + NST;   // [NSC] scales.  Slot i of tile t + NSC is written once
                                       // tile t + NSC - NST's S is done, hence after every
                                       // softmax of tile t
-  uint64_t* s_full = sc_full + NSC;   // QT 2: [QT] a tile's scores are there; QT 1: [2] a step's
+  uint64_t* s_full = sc_full + NSC;   // [2] the scores of a row tile's keys are there; ONE: of a step
   uint64_t* p_full = s_full + 4;      // [QT][2] its weights are written
   uint64_t* pv_done = p_full + 4;     // [QT] each step's O += P V is complete
   uint64_t* o_full = pv_done + 2;     // [QT] the last one is
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *s_tmem;
-  const int tiles = it.rows > 128 ? QT : 1;  // row tiles with rows
+  const int tiles = !ONE && it.rows > 128 ? QT : 1;  // row tiles with rows
   const int nt = it.t1 - it.t0;
 
   if (warp < Cfg::SMW) {
@@ -361,8 +363,10 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       const uint32_t t_h = t_lane + sb * UK;
       if (u % UPT == 0) {
         ok = paged_wait(&sc_full[sc], (i / NSC) & 1, p.err, (const volatile int*)s_abort) &&
-             (QT == 2 ? paged_wait(&s_full[j], i & 1, p.err, (const volatile int*)s_abort)
-                      : paged_wait(&s_full[u & 1], (u >> 1) & 1, p.err, (const volatile int*)s_abort));
+             (!ONE ? paged_wait(&s_full[j], i & 1, p.err, (const volatile int*)s_abort)
+                   : paged_wait(&s_full[u & 1], (u >> 1) & 1, p.err, (const volatile int*)s_abort));
+      } else if (ONE) {
+        ok = paged_wait(&s_full[u & 1], (u >> 1) & 1, p.err, (const volatile int*)s_abort);
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -673,19 +677,21 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     auto wait = [&](uint64_t* bar, uint32_t ph) {
       return (bool)__all_sync(0xffffffffu, paged_wait(bar, ph, p.err, (const volatile int*)s_abort));
     };
-    constexpr uint32_t idS = idesc_f16_f32(128, Cfg::SN, false);
+    constexpr uint32_t idS = idesc_f16_f32(128, ONE ? UK : KT, false);
     constexpr uint32_t idO = idesc_f16_f32(128, HD, true);
     const uint32_t qa = smem_u32(q_s), ka = smem_u32(k_s), va = smem_u32(v_s);
-    // S = Q K^T for row tile j: of tile x, or (QT 1) of step x, its tile
+    // S = Q K^T for row tile j: of tile x, or (ONE) of step x
     auto issue_s = [&](int x, int j) {
-      const uint32_t d = tmem + (QT == 2 ? 2 * j : x & 1) * UK;
+      const int tile = ONE ? x / UPT : x;
+      const uint32_t d = tmem + (ONE ? x & 1 : 2 * j) * UK;
       // descriptors count addresses in 16 bytes: steps are added to the first one
-      const uint64_t qd = smem_desc_sw128(qa + j * Cfg::QTILE), kd = smem_desc_sw128(ka + x % NST * Cfg::KTILE);
+      const uint64_t qd = smem_desc_sw128(qa + j * Cfg::QTILE),
+                     kd = smem_desc_sw128(ka + tile % NST * Cfg::KTILE + (ONE ? x % UPT * (UK * 128) : 0));
 #pragma unroll
       for (int kk = 0; kk < HD / 16; ++kk)
         mma_ss(d, qd + (((kk >> 2) * Cfg::QBOX + (kk & 3) * 32) >> 4),
                kd + (((kk >> 2) * Cfg::KBOX + (kk & 3) * 32) >> 4), idS, kk != 0);
-      mma_commit(&s_full[QT == 2 ? j : x & 1]);
+      mma_commit(&s_full[ONE ? x & 1 : j]);
     };
     // O += P V of step u, once its weights are there
     auto issue_pv = [&](int u, int j) {
@@ -701,7 +707,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       return true;
     };
     bool ok = wait(q_full, 0);
-    if (QT == 2) {
+    if (!ONE) {
       // tile i: P V of tile i - 1, then S of tile i over it, for one row tile while the other is
       // in its softmax
       for (int i = 0; ok && i <= nt; ++i) {
@@ -723,20 +729,24 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
         if (i < nt) mma_commit(&k_free[i % NST]);
       }
     } else {
-      // S of step i + 1 runs while step i is in its softmax
-      for (int i = -1; ok && i < nt; ++i) {
-        if (i + 1 < nt) {
-          ok = wait(&k_full[(i + 1) % NST], ((i + 1) / NST) & 1);
+      // S of step u + 1 runs while step u is in its softmax, over step u - 1
+      const int steps = nt * UPT;
+      for (int u = -1; ok && u < steps; ++u) {
+        if (u + 1 < steps) {
+          const int x = (u + 1) / UPT;
+          if ((u + 1) % UPT == 0) ok = wait(&k_full[x % NST], (x / NST) & 1);
           if (!ok) break;
           tc_fence_after();
-          issue_s(i + 1, 0);
-          mma_commit(&k_free[(i + 1) % NST]);
+          issue_s(u + 1, 0);
+          if ((u + 2) % UPT == 0) mma_commit(&k_free[x % NST]);
         }
-        if (i >= 0) {
-          ok = wait(&v_full[i % NST], (i / NST) & 1) && issue_pv(i, 0);
+        if (u >= 0) {
+          const int x = u / UPT;
+          if (u % UPT == 0) ok = wait(&v_full[x % NST], (x / NST) & 1);
+          ok = ok && issue_pv(u, 0);
           if (!ok) break;
-          if (i == nt - 1) mma_commit(&o_full[0]);
-          mma_commit(&v_free[i % NST]);
+          if (u == steps - 1) mma_commit(&o_full[0]);
+          if ((u + 1) % UPT == 0) mma_commit(&v_free[x % NST]);
         }
       }
     }
@@ -807,9 +817,12 @@ __global__ void __launch_bounds__(256) paged_block_merge_kernel(const PagedAttnA
 }
 
 template <int HD>
-cudaError_t launch_block_hd(const PagedAttnArgs& a, int slots, int splits, cudaStream_t s) {
+cudaError_t launch_block_hd(const PagedAttnArgs& a, int slots, int splits, bool one, cudaStream_t s) {
   using Cfg = BlockCfg<HD>;
-  auto kern = a.cap_log2 != 0.f ? paged_block_kernel<HD, true> : paged_block_kernel<HD, false>;
+  const bool cap = a.cap_log2 != 0.f;
+  auto kern = cap ? paged_block_kernel<HD, true, true> : paged_block_kernel<HD, false, true>;
+  if constexpr (Cfg::QT == 2)
+    if (!one) kern = cap ? paged_block_kernel<HD, true, false> : paged_block_kernel<HD, false, false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
   if (e != cudaSuccess) return e;
   const int units = slots * a.p.nkv;
@@ -823,10 +836,11 @@ cudaError_t launch_block_hd(const PagedAttnArgs& a, int slots, int splits, cudaS
 int paged_block_rows(int hd) { return hd == 256 ? BlockCfg<256>::ROWS : BlockCfg<128>::ROWS; }
 int paged_block_keys(int hd) { return hd == 256 ? BlockCfg<256>::KT : BlockCfg<128>::KT; }
 
-cudaError_t launch_paged_block(const PagedAttnArgs& a, int slots, int splits, cudaStream_t s) {
-  if (a.p.hd == 64) return launch_block_hd<64>(a, slots, splits, s);
-  if (a.p.hd == 128) return launch_block_hd<128>(a, slots, splits, s);
-  return launch_block_hd<256>(a, slots, splits, s);
+cudaError_t launch_paged_block(const PagedAttnArgs& a, int slots, int splits, int max_rows, cudaStream_t s) {
+  const bool one = max_rows <= 128;
+  if (a.p.hd == 64) return launch_block_hd<64>(a, slots, splits, one, s);
+  if (a.p.hd == 128) return launch_block_hd<128>(a, slots, splits, one, s);
+  return launch_block_hd<256>(a, slots, splits, one, s);
 }
 
 }  // namespace hfa
