@@ -480,7 +480,8 @@ hfa_status hfa_paged_append(hfa_paged* paged, void* stream, int batch, const int
  *   o = sum_p softmax_p(attn_scale * q . k_p [softcap]) v_p.
  * A row that sees nothing (P < 0) gives zeros.
  *   len_dev / len_host  int32 [batch], 0 <= len <= max_pages * page_size (HFA_ERANGE)
- *   q_dev   [T, nh, hd], rows q_stride elements apart; o_dev dense [T, nh, hd]
+ *   q_dev   [T, nh, hd], rows q_stride elements apart; o_dev dense [T, nh, hd], not
+ *           overlapping q_dev
  *   dtype   of q and o.  HFA_F32 is for few rows: n * nh / nkv <= 8 in every sequence
  *           (HFA_EUNSUPPORTED otherwise); with HFA_BF16 n is free.
  *   workspace_dev  hfa_paged_workspace_bytes(paged, batch, T) bytes, 16-byte aligned, zero

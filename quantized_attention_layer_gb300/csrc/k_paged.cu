@@ -11,8 +11,8 @@
 // the page rotate the queries, four heads' loads in flight together.  A thread holds 8 values
 // of a row, 4 of each half, so both members of its pairs are its own, and few registers: four
 // CTAs of 256 threads share an SM, one loading while another computes (with 16 values a thread
-// and 16 warps an SM an 8K prompt took 53 us).  Memory-bound by design; the issue slots come
-// next (about 20 instructions a value).
+// and 16 warps an SM an 8K prompt took 53 us for 47, 3.9 TB/s).  Memory-bound by design; the
+// issue slots come next (about 20 instructions a value).
 #include "hfa_common.cuh"
 #include "hfa_finish.cuh"
 #include "hfa_internal.h"
@@ -418,7 +418,8 @@ cudaError_t launch_append_t(const PagedAppendArgs& a, dim3 grid, int threads, bo
 
 // Read: one CTA decodes one page's rows of some KV heads; a thread takes the 8 codes of chunk
 // c of rows r, r + 256 / U, ...: one 8-byte load and one 16-byte store each, so that a warp's
-// store is 512 whole bytes, four rows' loads in flight.  Memory-bound.
+// store is 512 whole bytes, four rows' loads in flight.  Memory-bound: 32K tokens (8 heads, hd
+// 128, 201 MB) 38 us, 5.2 TB/s.
 template <int HD>
 __global__ void __launch_bounds__(256) paged_read_kernel(const PagedReadArgs a) {
   constexpr int U = HD / 8, RP = 256 / U, NB = 4;

@@ -25,6 +25,9 @@
 // a score exceeds it by 2^8, which a warp vote finds without any shuffle.  The V scale enters
 // in the exponent: weights are w = 2^(s + log2 vs - mw) with a maximum mw of their own, the
 // denominator l = sum 2^(s - m): fp16 weights then keep their bits whatever the pages' scales.
+//
+// 4 sequences of 128K keys (40/8 heads, hd 128, 1.07 GB): 195 us, 5.5 TB/s; 64 ragged ones of up
+// to 8K (473 MB) 99.7 us, 4.7 TB/s: what a unit costs beside its blocks (below) is the rest.
 #include "hfa_common.cuh"
 #include "hfa_internal.h"
 #include "hfa_paged.h"
