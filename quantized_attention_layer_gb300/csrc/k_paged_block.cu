@@ -41,10 +41,11 @@
 namespace hfa {
 namespace {
 
-template <int HD>
+// ONE: no CTA of the call has more than one row tile
+template <int HD, bool ONE = HD == 256>
 struct BlockCfg {
-  static constexpr int QT = HD == 256 ? 1 : 2;    // row tiles of a CTA
-  static constexpr int ROWS = QT * 128;
+  static constexpr int QT = ONE ? 1 : 2;          // row tiles of a CTA
+  static constexpr int ROWS = HD == 256 ? 128 : 256;  // rows that the CTAs are dealt out by
   static constexpr int KT = HD == 256 ? 64 : 128; // keys of a tile
   static constexpr int NG = KT / 16;              // 16-key groups: one scale each
   static constexpr int UK = 64, UPT = KT / UK;    // keys of a softmax step, steps of a tile
@@ -65,6 +66,8 @@ struct BlockCfg {
   static constexpr int RPU = 32 / CPR;            // rows of a converter's unit: 32 chunks
   static constexpr int NU = KT / RPU;             // units of a tile
   static constexpr int PER = (NU + NCW - 1) / NCW;  // units of one warp
+  // tiles of codes in a converter's registers: with one row tile the conversion sets the pace
+  static constexpr int DEPTH = ONE ? 2 : 1;
   static_assert(O_COL + QT * HD <= 512, "TMEM");
   static_assert(16 % RPU == 0, "a unit lies in one group");
   static_assert(SMEM <= 232448, "shared memory");
@@ -211,9 +214,9 @@ __device__ __forceinline__ bool block_item(const PagedAttnArgs& a, int splits, i
 // tile's work does, and scores come by whole tiles (by steps they read Q twice).  16 rows of 4
 // sequences over 8K keys take 32.5 us by steps and 37.5 by tiles, an 8K prompt 458 and 412.
 template <int HD, bool CAP, bool ONE>
-__global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
+__global__ void __launch_bounds__(BlockCfg<HD, ONE>::THREADS, 1)
     paged_block_kernel(const PagedAttnArgs a, int splits) {
-  using Cfg = BlockCfg<HD>;
+  using Cfg = BlockCfg<HD, ONE>;
   constexpr int QT = Cfg::QT, KT = Cfg::KT, NG = Cfg::NG, UK = Cfg::UK, UPT = Cfg::UPT, HG = UK / 16, NST = Cfg::NST, NSC = Cfg::NSC;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_align1024(smem_raw);
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
     // tile l / NG: a warp that uses a load's result may wait for every later load too (they share
     // scoreboards), so that happens twice a batch and not twice a tile
     constexpr int TB = 32 / NG;
-    static_assert(TB >= 4, "entries, rows and scales are two tiles apart");
+    static_assert(TB >= 4 && TB - Cfg::DEPTH >= 2, "entries, rows and scales are two tiles apart");
     auto key_of = [&](int batch) { return (it.t0 + batch * TB + lane / NG) * KT + 16 * (lane % NG); };
     auto wanted = [&](int batch) {
       return batch * TB + lane / NG < nt && key_of(batch) < it.hi && key_of(batch) + 16 > it.lo;
@@ -609,16 +612,21 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
         v = ld_global(p.v_scales + (gr >> p.ps_log2));
       }
     };
-    // in flight: the codes of tile i + 1, the rows and scales of the next batch
-    uint4 kw[PER], vw[PER];
+    // in flight: the codes of DEPTH tiles, the rows and scales of the next batch
+    constexpr int DEPTH = Cfg::DEPTH;
+    uint4 kws[DEPTH][PER], vws[DEPTH][PER];
     float ks, vs, ks1 = 0.f, vs1 = 0.f;
     int pg1 = 0;
     int grow = group_row(0, fetch_page(0)), grow1 = -1;
-    load(p.k_codes, grow, 0, kw);
-    load(p.v_codes, grow, 0, vw);
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+      load(p.k_codes, grow, d, kws[d]);
+      load(p.v_codes, grow, d, vws[d]);
+    }
     scales(grow, ks, vs);
     const bool lead = cw == 0;
-    for (int i = 0; i < nt; ++i) {
+    // tile i: false when a wait gave up
+    auto convert = [&](int i, uint4 (&kw)[PER], uint4 (&vw)[PER]) {
       const int st = i % NST, sc = i % NSC, bt = i % TB;
       const uint32_t ph = ((i / NST) & 1) ^ 1;
       if (bt == 0) {
@@ -628,13 +636,10 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
         grow1 = group_row(i / TB + 1, pg1);
         scales(grow1, ks1, vs1);
       }
-      const int grow_ahead = bt == TB - 1 ? grow1 : grow;  // of the batch of tile i + 1
+      const int grow_ahead = bt >= TB - DEPTH ? grow1 : grow;  // of the batch of tile i + DEPTH
       bool ok = i < NST || paged_wait(&k_free[st], ph, p.err, (const volatile int*)s_abort);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {
-        *s_abort = 1;
-        break;
-      }
+      if (!ok) return false;
       const bool mine = lane / NG == bt;  // this lane's group is of tile i
       if (lead) {
         const bool any_bad = __any_sync(0xffffffffu, mine && grow == -2);
@@ -654,13 +659,10 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&k_full[st]);
-      load(p.k_codes, grow_ahead, i + 1, kw);
+      load(p.k_codes, grow_ahead, i + DEPTH, kw);
       ok = i < NST || paged_wait(&v_free[st], ph, p.err, (const volatile int*)s_abort);
       ok = __all_sync(0xffffffffu, ok);
-      if (!ok) {
-        *s_abort = 1;
-        break;
-      }
+      if (!ok) return false;
       // pages with V scale 0 count as zeros, whatever their codes
       const uint32_t zero = __ballot_sync(0xffffffffu, mine && grow >= 0 && !(vs > 0.f)) >> (bt * NG);
       if (zero) {
@@ -672,7 +674,17 @@ __global__ void __launch_bounds__(BlockCfg<HD>::THREADS, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&v_full[st]);
-      load(p.v_codes, grow_ahead, i + 1, vw);
+      load(p.v_codes, grow_ahead, i + DEPTH, vw);
+      return true;
+    };
+    for (int i = 0; i < nt; i += DEPTH) {
+      bool ok = true;
+#pragma unroll
+      for (int d = 0; d < DEPTH; ++d) ok = ok && (i + d >= nt || convert(i + d, kws[d], vws[d]));
+      if (!ok) {
+        *s_abort = 1;
+        break;
+      }
     }
   } else {
     // ================================================================== MMA issuer
@@ -824,12 +836,16 @@ cudaError_t launch_block_hd(const PagedAttnArgs& a, int slots, int splits, bool 
   using Cfg = BlockCfg<HD>;
   const bool cap = a.cap_log2 != 0.f;
   auto kern = cap ? paged_block_kernel<HD, true, true> : paged_block_kernel<HD, false, true>;
+  size_t smem = BlockCfg<HD, true>::SMEM;
   if constexpr (Cfg::QT == 2)
-    if (!one) kern = cap ? paged_block_kernel<HD, true, false> : paged_block_kernel<HD, false, false>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg::SMEM);
+    if (!one) {
+      kern = cap ? paged_block_kernel<HD, true, false> : paged_block_kernel<HD, false, false>;
+      smem = Cfg::SMEM;
+    }
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int units = slots * a.p.nkv;
-  e = paged_launch(kern, dim3((unsigned)(units * splits)), Cfg::THREADS, Cfg::SMEM, s, a, splits);
+  e = paged_launch(kern, dim3((unsigned)(units * splits)), Cfg::THREADS, smem, s, a, splits);
   if (e != cudaSuccess || splits == 1) return e;
   return paged_launch(paged_block_merge_kernel<HD>, dim3((unsigned)(units * (Cfg::ROWS / 8))), 256, 0, s, a, splits);
 }
