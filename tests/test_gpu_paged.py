@@ -315,6 +315,19 @@ def test_attention_blocks_window_softcap_bidirectional(hd, ps, G, window, softca
                   softcap=softcap, scale=0.2, bidir=bidir, repeat=2)
 
 
+@pytest.mark.parametrize("hd,ps,nkv,G,window,softcap,bidir", [
+    (64, 16, 3, 4, 0, 0.0, False), (128, 32, 2, 4, 0, 0.0, False), (128, 16, 1, 2, 33, 0.0, False),
+    (64, 128, 2, 3, 300, 20.0, False), (128, 64, 40, 4, 0, 0.0, True), (128, 128, 2, 1, 0, 30.0, False),
+    (64, 32, 50, 4, 17, 0.0, False)])
+def test_attention_blocks_of_one_row_tile(hd, ps, nkv, G, window, softcap, bidir):
+    """Every sequence has at most 128 rows x heads, one of them just that many; few items that
+    CTAs share, and more items than that."""
+    ns = [128 // G, 16, 0, 9, 1, 30]
+    lens = [700, 1300, 50, 9, 200, 28 if not bidir else 64]
+    run_attention(hd + ps + G, nkv * G, nkv, hd, ps, ns, lens, torch.bfloat16, window=window, softcap=softcap,
+                  scale=0.2, bidir=bidir, repeat=2)
+
+
 @pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
 def test_attention_long_single_sequence(kind):
     run_attention(1, 8, 2, 128, 64, [1], [20000], kind, repeat=2)
@@ -809,3 +822,48 @@ def test_refuses_tensors_off_the_device():
     off(p.hfa_paged_attention, [cud, cu, ld, ln, x, pool.pages, ws, x.clone()])
     off(p.hfa_paged_read, [zd, z, ld, ln, pool.pages, cache, cache.clone()])
     p.hfa_paged_check_status()
+
+
+@pytest.mark.parametrize("hd", [64, 128, 256])
+def test_the_largest_batch(hd):
+    """4096 sequences, some without rows, some with none of their positions visible."""
+    rng = np.random.default_rng(81)
+    ns = [0 if b % 7 == 3 else 2 if b % 11 == 5 else 1 for b in range(4096)]
+    lens = rng.integers(0, 48, 4096)
+    lens[4095] = 700
+    run_attention(81 + hd, 2, 1, hd, 16, ns, lens, torch.bfloat16)
+    with pytest.raises(hfa.HfaError) as e:
+        run_attention(81 + hd, 2, 1, hd, 16, ns + [1], list(lens) + [3], torch.bfloat16, poison=False)
+    assert e.value.status == hfa.HFA_EINVAL
+
+
+def test_the_largest_batch_appended_and_read():
+    rng = np.random.default_rng(82)
+    B, nkv, hd, ps, mx = 4096, 1, 64, 16, 3
+    ns = np.array([0 if b % 5 == 2 else 1 + b % 3 for b in range(B)], dtype=np.int32)
+    start = rng.integers(0, mx * ps - 3, B).astype(np.int32)
+    cu = ref.ragged(ns)
+    T = int(cu[-1])
+    table, num = ref.make_table(rng, [mx] * B, mx)
+    arrays = ref.make_pool(rng, num, nkv, ps, hd)
+    pool = Pool(arrays, table)
+    p = make(nkv, nkv, hd, ps, num, mx)
+    x = draw_rows(rng, T, 2, hd, torch.float32)
+    xd = x.cuda()
+    p.hfa_paged_append(ref.dev(cu), cu, ref.dev(start), start, None, xd[:, :1], xd[:, 1:], pool.pages)
+    p.hfa_paged_check_status()
+    after = pool.host()
+    pos = np.concatenate([start[b] + np.arange(ns[b]) for b in range(B)])
+    xf = x.double().numpy()
+    check_appended(arrays[:2], after[:2], ref.rotate_rows(xf[:, :1], pos, 1e4, None), cu, start, table, ps)
+    check_appended(arrays[2:], after[2:], xf[:, 1:], cu, start, table, ps)
+    kc = torch.zeros((B, nkv, mx * ps, hd), dtype=torch.bfloat16, device="cuda")
+    vc = torch.zeros_like(kc)
+    p.hfa_paged_read(ref.dev(start), start, ref.dev(ns), ns, pool.pages, kc, vc)
+    p.hfa_paged_check_status()
+    seq = np.repeat(np.arange(B), ns)
+    pg = table[seq, pos // ps]
+    for got, codes, scales in ((kc, after[0], after[1]), (vc, after[2], after[3])):
+        want = torch.from_numpy(codes[pg, 0, pos % ps].astype(np.float32) * scales[pg, 0][:, None]).to(torch.bfloat16)
+        assert torch.equal(got.cpu()[seq, 0, pos], want)
+        assert int((got != 0).any(-1).sum()) <= T
